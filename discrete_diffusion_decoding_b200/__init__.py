@@ -12,13 +12,17 @@ import torch
 
 from . import _abi
 from ._abi import DgError, DgParams, check, lib
+from .training import (AdamW, AdamWTensors, HeadTrainer, XentWorkspace, adamw_params, dg_adamw_step,
+                       dg_xent_backward, dg_xent_forward, head_cross_entropy, xent_params, xent_workspace_size)
 
 __all__ = ["DgError", "DgParams", "params", "workspace_size", "plan", "temperature", "dg_canvas_init",
            "dg_denoise_step", "dg_stop_check", "dg_stub_hidden", "last_launch_count", "profile_enable",
            "profile_collect", "dg_denoise_stats_noalloc", "dg_debug_set_error", "Workspace", "StepBuffers",
            "decode_batch", "decode_block_ar", "dg_partial_bytes", "dg_denoise_partial", "dg_denoise_merge",
            "dg_debug_set_counter_wait_limit", "dg_quantize_e4m3", "quantize_head_e4m3", "dg_last_sm_clock",
-           "dg_tile_head", "tile_head"]
+           "dg_tile_head", "tile_head", "xent_params", "xent_workspace_size", "XentWorkspace", "dg_xent_forward",
+           "dg_xent_backward", "head_cross_entropy", "adamw_params", "AdamWTensors", "dg_adamw_step", "AdamW",
+           "HeadTrainer"]
 
 
 def params(n_canvas, vocab, hidden, **overrides):

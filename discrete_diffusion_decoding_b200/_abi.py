@@ -13,7 +13,11 @@ EXPORTS = ("dg_params_default", "dg_temperature", "dg_workspace_size", "dg_canva
            "dg_stop_check", "dg_stub_hidden", "dg_status_string", "dg_last_launch_count", "dg_plan",
            "dg_profile_enable", "dg_profile_collect", "dg_denoise_stats_noalloc", "dg_debug_set_error",
            "dg_partial_bytes", "dg_denoise_partial", "dg_denoise_merge", "dg_debug_set_counter_wait_limit",
-           "dg_quantize_e4m3", "dg_last_sm_clock", "dg_tile_head")
+           "dg_quantize_e4m3", "dg_last_sm_clock", "dg_tile_head", "dg_xent_params_default",
+           "dg_xent_workspace_size", "dg_xent_forward", "dg_xent_backward", "dg_adamw_params_default", "dg_adamw_step")
+
+DG_FP32, DG_BF16 = 0, 1
+DG_INT32, DG_INT64 = 0, 1
 
 
 class DgParams(ctypes.Structure):
@@ -23,6 +27,27 @@ class DgParams(ctypes.Structure):
                 ("stability", ctypes.c_int), ("tied", ctypes.c_int), ("group", ctypes.c_int),
                 ("accept_mode", ctypes.c_int), ("accept_rule", ctypes.c_int), ("logits_format", ctypes.c_int),
                 ("w_scale_exp", ctypes.c_int), ("head_layout", ctypes.c_int)]
+
+
+class DgXentParams(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int), ("vocab", ctypes.c_int), ("hidden", ctypes.c_int),
+                ("temperature", ctypes.c_float), ("ignore_index", ctypes.c_longlong),
+                ("h_stride", ctypes.c_longlong), ("target_type", ctypes.c_int), ("dw_type", ctypes.c_int),
+                ("dw_accumulate", ctypes.c_int)]
+
+
+class DgAdamWParams(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("seed", ctypes.c_uint64), ("lr_dev", ctypes.c_void_p),
+                ("step_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p),
+                ("grad_scale", ctypes.c_float), ("step", ctypes.c_int), ("state_bits", ctypes.c_int),
+                ("param_type", ctypes.c_int), ("grad_type", ctypes.c_int), ("stochastic", ctypes.c_int)]
+
+
+class DgAdamWTensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("n", ctypes.c_longlong), ("weight_decay", ctypes.c_float)]
 
 
 class DgError(RuntimeError):
@@ -82,6 +107,19 @@ def lib():
         L.dg_last_sm_clock.restype = i32
         L.dg_tile_head.argtypes = [vp, vp, ctypes.c_longlong, i32, i32, vp]
         L.dg_tile_head.restype = i32
+        X = ctypes.POINTER(DgXentParams)
+        L.dg_xent_params_default.argtypes = [X, i32, i32, i32]
+        L.dg_xent_params_default.restype = None
+        L.dg_xent_workspace_size.argtypes = [X, i32]
+        L.dg_xent_workspace_size.restype = sz
+        L.dg_xent_forward.argtypes = [X, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dg_xent_forward.restype = i32
+        L.dg_xent_backward.argtypes = [X, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+        L.dg_xent_backward.restype = i32
+        L.dg_adamw_params_default.argtypes = [ctypes.POINTER(DgAdamWParams)]
+        L.dg_adamw_params_default.restype = None
+        L.dg_adamw_step.argtypes = [ctypes.POINTER(DgAdamWParams), ctypes.POINTER(DgAdamWTensor), i32, vp]
+        L.dg_adamw_step.restype = i32
         L.dg_profile_enable.argtypes = [i32]
         L.dg_profile_enable.restype = i32
         L.dg_profile_collect.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(ctypes.c_float),

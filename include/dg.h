@@ -248,8 +248,9 @@ dg_status dg_stub_hidden(const dg_params* p, int step, float gain, float noise, 
 const char* dg_status_string(dg_status s);
 
 /* Number of kernel launches the last launching call (dg_canvas_init, dg_denoise_step,
- * dg_stub_hidden, dg_denoise_partial, dg_denoise_merge, dg_denoise_stats_noalloc) on this
- * host thread issued; 0 when it failed before launching. */
+ * dg_stub_hidden, dg_denoise_partial, dg_denoise_merge, dg_denoise_stats_noalloc,
+ * dg_xent_forward, dg_xent_backward, dg_adamw_step) on this host thread issued; 0 when it
+ * failed before launching. */
 int dg_last_launch_count(void);
 
 /*
@@ -362,6 +363,134 @@ dg_status dg_tile_head(const void* src_dev, void* dst_dev, long long rows, int c
  */
 dg_status dg_quantize_e4m3(const void* src_dev, long long rows, int cols, int per_row, uint8_t* codes_dev,
                            int32_t* exps_dev, void* stream);
+
+/* ------------------------------------------------------------------ training the head
+ * The softmax cross entropy of the same vocabulary head with its gradients, and the AdamW
+ * step that applies them.  Neither is on the pages, which describe inference only; the
+ * conventions at the top of this file hold (caller-owned memory, asynchronous on `stream`,
+ * argument errors before anything is launched).  Calls that may run at the same time need a
+ * workspace each; a captured graph keeps using the one that it was captured with. */
+
+/* Element types of the training entry points. */
+enum { DG_FP32 = 0, DG_BF16 = 1 };
+enum { DG_INT32 = 0, DG_INT64 = 1 };
+
+/*
+ * Cross entropy of a head W [vocab, hidden] at n positions.  Limits: n >= 0, vocab >= 1,
+ * temperature > 0 and finite (DG_EINVAL otherwise); hidden a multiple of 8 up to 65536,
+ * n up to 2^22, vocab up to 2^28 (DG_EUNSUPPORTED otherwise).
+ */
+typedef struct {
+    int n;                  /* positions */
+    int vocab;              /* V */
+    int hidden;             /* d */
+    float temperature;      /* T: z = h W^T / T */
+    long long ignore_index; /* targets with this value take no part */
+    long long h_stride;     /* elements between the rows of h; 0 = hidden */
+    int target_type;        /* DG_INT32 or DG_INT64 */
+    int dw_type;            /* type of dW: DG_BF16 or DG_FP32 */
+    int dw_accumulate;      /* 1: dW is added to what dW_dev holds; 0: it overwrites it */
+} dg_xent_params;
+
+/* temperature 1, ignore_index -100, dense h, int32 targets, bf16 dW, overwrite. */
+void dg_xent_params_default(dg_xent_params* p, int n, int vocab, int hidden);
+
+/* Bytes of workspace for p on the current device (256-byte aligned memory): of the forward,
+ * or with `backward` 1 of both directions.  0 if p is invalid or unsupported. */
+size_t dg_xent_workspace_size(const dg_xent_params* p, int backward);
+
+/*
+ * Per-position loss, without storing logits: for every position i whose target is not
+ * ignore_index
+ *   lse_i = ln sum_v e^{z[i,v]},  loss_i = lse_i - z[i, y_i]   (nats, fp32)
+ * computed so that small losses keep their relative precision.  Ignored positions get
+ * loss 0 and lse 0 and cost nothing; their hidden states may hold anything.  A target
+ * outside [0, vocab) that is not ignore_index gives NaN, and so do logits that are not finite.
+ *   h_dev:       [n, hidden] bf16, rows h_stride apart (any alignment; 16 bytes is faster)
+ *   W_dev:       [vocab, hidden] bf16, row-major, 16-byte aligned
+ *   targets_dev: [n] int32 or int64
+ *   loss_dev, lse_dev: [n] float (written; lse may be NULL)
+ * n = 0 does nothing.  Three launches.  A wait that runs out makes every loss and lse NaN.
+ */
+dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void* W_dev, const void* targets_dev,
+                          float* loss_dev, float* lse_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of sum_i dloss_i loss_i, from the forward's loss and lse of the same inputs:
+ *   G[i,v] = dloss_i / T (e^{z[i,v] - lse_i} - [v = y_i]),  dh = G W,  dW = G^T h
+ * with the logits computed again, a piece of the vocabulary at a time; G is rounded to
+ * bf16 for the two products, whose sums are fp32.  Ignored positions and those with
+ * dloss_i = 0 get a zero row of dh and no part in dW, whatever their hidden states hold.
+ * An invalid target (see dg_xent_forward) makes its row of dh and all of dW NaN.
+ *   dloss_dev: [n] float
+ *   dh_dev:    [n, hidden] bf16, 16-byte aligned (NULL: not wanted)
+ *   dW_dev:    [vocab, hidden] bf16 or fp32 (dw_type), 16-byte aligned (NULL: not wanted)
+ * At least one of dh_dev and dW_dev (DG_EINVAL); neither may overlap W, nor dh h (DG_EINVAL).
+ * n = 0 zeroes dW unless dw_accumulate.  The results of equal calls are equal to the bit.
+ * A wait that runs out makes both gradients NaN.
+ */
+dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const void* W_dev, const void* targets_dev,
+                           const float* loss_dev, const float* lse_dev, const float* dloss_dev, void* dh_dev,
+                           void* dW_dev, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
+ * AdamW with decoupled weight decay over a list of tensors, in one launch per 400 tensors.
+ * Per element, with g' = grad_scale * g and step t:
+ *   m <- beta1 m + (1 - beta1) g'      v <- beta2 v + (1 - beta2) g'^2
+ *   p <- p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ * in fp32.  state_bits 32: m and v are fp32 [n].  state_bits 8: m and v are E4M3 codes [n]
+ * of m and of sqrt(v), with one power-of-two exponent (int8) for every 256 consecutive
+ * elements, value = decode(code) 2^exp; the exponent is the smallest with max |x| 2^-exp <= 448
+ * (0 for a block of zeros, at least -100), and codes are rounded between their two E4M3
+ * neighbours at random: up when floor(x 2^-exp / spacing + u / 2^16) says so, u 16 random
+ * bits; a positive sqrt(v) is stored as at least the smallest code, a non-finite value as NaN.
+ * All-zero codes and exponents are the zero state.
+ * bf16 parameters: with `master` (fp32) the update happens there and param is its rounding
+ * to nearest; without, param is rounded to nearest, or with `stochastic` 1 at random (u added
+ * to the low 16 bits of the fp32 value, then cut).
+ * Random words: Philox4x32-10, key = seed, counter = (element / 4, step, tensor's place in
+ * the list, 5), word j for element 4 q + j, low half for m, high half for sqrt(v); for
+ * parameters counter (element / 8, step, place, 6), word j for elements 8 q + 2 j (low) and
+ * 8 q + 2 j + 1 (high).  Equal calls give equal bits.
+ * With lr_dev / step_dev / grad_scale_dev (device scalars, may be NULL) lr and step are read
+ * there when the kernel runs, and grad_scale is multiplied by that value, so a captured
+ * step can be replayed with other values.
+ */
+typedef struct {
+    double lr, beta1, beta2, eps;   /* lr, eps >= 0; betas in [0, 1) */
+    uint64_t seed;
+    const float* lr_dev;
+    const int32_t* step_dev;
+    const float* grad_scale_dev;
+    float grad_scale;
+    int step;                       /* t >= 1 (not read with step_dev) */
+    int state_bits;                 /* 8 or 32 */
+    int param_type, grad_type;      /* DG_FP32 or DG_BF16, of every tensor of the call */
+    int stochastic;                 /* bf16 parameters without master only */
+} dg_adamw_params;
+
+typedef struct {
+    void* param;            /* [n] (read and written; with master only written) */
+    const void* grad;       /* [n] (read) */
+    void* m;                /* [n] fp32 or uint8 codes (read and written) */
+    void* v;
+    int8_t* m_exp;          /* [ceil(n / 256)], state_bits 8 only */
+    int8_t* v_exp;
+    float* master;          /* [n] fp32 or NULL: for all tensors of a call or for none */
+    long long n;            /* 0 <= n < 2^34 */
+    float weight_decay;
+} dg_adamw_tensor;
+
+/* lr 1e-3, betas 0.9 and 0.999, eps 1e-8, grad_scale 1, step 1, 32-bit states, bf16, to nearest. */
+void dg_adamw_params_default(dg_adamw_params* p);
+
+/*
+ * `tensors` is a host array, read before the call returns; what its device pointers name must
+ * not overlap.  Dense arrays of natural alignment; 32-byte aligned ones are faster.
+ * Errors: DG_EINVAL (null or misaligned pointers, values outside the ranges above, master
+ * beside fp32 parameters or with stochastic), DG_ECUDA.
+ */
+dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors, int n_tensors, void* stream);
 
 /* Column-slice group size and group count the fused kernel uses for p on the current device. */
 dg_status dg_plan(const dg_params* p, int* group, int* n_groups, int* slice_cols);
