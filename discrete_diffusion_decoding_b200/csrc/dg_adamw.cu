@@ -26,6 +26,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "../../include/dg.h"
 #include "dg_common.cuh"
@@ -37,6 +38,7 @@ namespace {
 
 constexpr int kBlock = 256;           // elements that share an exponent: one warp, 8 a lane
 constexpr int kWarps = 8;
+constexpr int kMaxBlocksPerWarp = 8;
 constexpr int kMinExp = -100;         // 2^-e and 2^(e - 9) stay normal
 constexpr uint32_t kTagState = 5, kTagParam = 6;
 constexpr int kFewTensors = 24;       // the short list's argument is under 2 KB
@@ -51,9 +53,27 @@ struct Tensor {
     int8_t* v_exp;
     float* master;
     long long n;
-    float weight_decay;
+    float decay;                      // 1 - lr wd; wd itself when lr or the step is on the device
     int aligned;                      // every pointer allows the 8-element accesses
 };
+
+// Philox4x32-10 (see dg_common.cuh) with the keys of its rounds made on the host: read from the
+// kernel's constants they cost neither registers nor the additions.
+struct Keys {
+    uint32_t k[10][2];
+};
+
+__device__ __forceinline__ void philox(uint32_t (&c)[4], const Keys& keys) {
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t p0 = static_cast<uint64_t>(0xD2511F53u) * c[0];
+        const uint64_t p1 = static_cast<uint64_t>(0xCD9E8D57u) * c[2];
+        c[0] = static_cast<uint32_t>(p1 >> 32) ^ c[1] ^ keys.k[r][0];
+        c[1] = static_cast<uint32_t>(p1);
+        c[2] = static_cast<uint32_t>(p0 >> 32) ^ c[3] ^ keys.k[r][1];
+        c[3] = static_cast<uint32_t>(p0);
+    }
+}
 
 template <int kCap>
 struct Args {
@@ -64,127 +84,394 @@ struct Args {
     const float* lr_dev;
     const int32_t* step_dev;
     const float* grad_scale_dev;
-    uint32_t seed_lo, seed_hi, step, first_tensor;
+    uint32_t step, first_tensor;
     int stochastic, n_tensors, blocks_per_warp;
+    Keys keys;
     Tensor t[kCap];
     int first_cta[kCap + 1];
 };
 
-// 8 elements of a lane as fp32 <-> memory, `live` of them in range (8 with vectors only).
-__device__ __forceinline__ void load8(const float* p, bool vec, int live, float (&x)[8]) {
-    if (vec) {
-        asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+// A lane's 8 elements as they lie in memory: 2 (codes), 4 (bf16) or 8 (fp32) words, in one access when
+// kVec, else element by element with `live` of them in range (the others 0).
+template <class T>
+struct Raw8 {
+    uint32_t w[2 * sizeof(T)];
+};
+
+template <bool kVec, class T>
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* p, int live) {
+    if constexpr (kVec && sizeof(T) == 4) {
+        asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]),
+                       "=r"(r.w[6]), "=r"(r.w[7])
                      : "l"(p));
+    } else if constexpr (kVec && sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = u.x, r.w[1] = u.y, r.w[2] = u.z, r.w[3] = u.w;
+    } else if constexpr (kVec) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = u.x, r.w[1] = u.y;
     } else {
+        constexpr int per = 4 / sizeof(T), bits = 8 * sizeof(T);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < live ? p[i] : 0.f;
+        for (int i = 0; i < 8 / per; ++i) r.w[i] = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live) {
+                uint32_t x;
+                if constexpr (sizeof(T) == 4) x = reinterpret_cast<const uint32_t*>(p)[i];
+                else if constexpr (sizeof(T) == 2) x = reinterpret_cast<const uint16_t*>(p)[i];
+                else x = reinterpret_cast<const uint8_t*>(p)[i];
+                r.w[i / per] |= x << (bits * (i % per));
+            }
     }
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, bool vec, int live, float (&x)[8]) {
-    if (vec) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(u[i] << 16);
-            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < live ? __bfloat162float(p[i]) : 0.f;
-    }
-}
-
-__device__ __forceinline__ void store8(float* p, bool vec, int live, const float (&x)[8]) {
-    if (vec) {
-        asm volatile("st.global.v8.f32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]),
-                     "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "l"(p)
+template <bool kVec, class T>
+__device__ __forceinline__ void store8(T* p, const Raw8<T>& r, int live) {
+    if constexpr (kVec && sizeof(T) == 4) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+                     "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7]), "l"(p)
                      : "memory");
+    } else if constexpr (kVec && sizeof(T) == 2) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else if constexpr (kVec) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
     } else {
+        constexpr int per = 4 / sizeof(T), bits = 8 * sizeof(T);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = x[i];
+            if (i < live) {
+                const uint32_t x = r.w[i / per] >> (bits * (i % per));
+                if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[i] = x;
+                else if constexpr (sizeof(T) == 2) reinterpret_cast<uint16_t*>(p)[i] = static_cast<uint16_t>(x);
+                else reinterpret_cast<uint8_t*>(p)[i] = static_cast<uint8_t>(x);
+            }
     }
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, bool vec, int live, const float (&x)[8]) {
-    if (vec) {
-        uint32_t u[4];
+__device__ __forceinline__ void to_floats(const Raw8<float>& r, float (&x)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = __float2bfloat16_rn(x[i]);
-    }
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
 }
 
-// 8 codes of a lane as two words.
-__device__ __forceinline__ void load_codes(const uint8_t* p, bool vec, int live, uint32_t (&c)[2]) {
-    if (vec) {
-        const uint2 w = *reinterpret_cast<const uint2*>(p);
-        c[0] = w.x;
-        c[1] = w.y;
-    } else {
-        c[0] = c[1] = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) c[i >> 2] |= static_cast<uint32_t>(p[i]) << (8 * (i & 3));
-    }
-}
-
-__device__ __forceinline__ void store_codes(uint8_t* p, bool vec, int live, const uint32_t (&c)[2]) {
-    if (vec) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(c[0], c[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < live) p[i] = static_cast<uint8_t>(c[i >> 2] >> (8 * (i & 3)));
-    }
-}
-
-// x = E4M3 codes times 2^e (exact: e >= -100 keeps every product normal).
-__device__ __forceinline__ void decode8(const uint32_t (&c)[2], int e, float (&x)[8]) {
-    const float scale = __int_as_float((e + 127) << 23);
+__device__ __forceinline__ void to_floats(const Raw8<__nv_bfloat16>& r, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>(c[i >> 1] >> (16 * (i & 1)));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
+        x[2 * i] = __uint_as_float(r.w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
     }
 }
 
-// The exponent of a block whose lane maxima of |x| (finite ones only) are `peak`: the smallest e
-// with max 2^-e <= 448 = 1.75 2^8 (a significand above 1.75 takes the next exponent).
-__device__ __forceinline__ int block_exponent(float peak) {
-    const int bits = __reduce_max_sync(0xffffffffu, __float_as_int(peak));
+__device__ __forceinline__ void from_floats(Raw8<float>& r, const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(x[i]);
+}
+
+__device__ __forceinline__ void from_floats(Raw8<__nv_bfloat16>& r, const float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+}
+
+// Two fp32 values in one register pair: sm_100 multiplies and adds both in one instruction, each
+// rounded by itself.
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ f32x2 pack2(float lo, float hi) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void unpack2(f32x2 x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Largest |x|, NaN when one of them is NaN.
+__device__ __forceinline__ float peak3(float peak, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(peak), "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float sqrt_sfu(float x) {
+    float r;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float div_sfu(float a, float b) {
+    float r;
+    asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
+
+// The E4M3 values of a lane's 8 codes.
+__device__ __forceinline__ void decode8(const Raw8<uint8_t>& c, f32x2 (&x)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_fp8x2_storage_t pair = static_cast<__nv_fp8x2_storage_t>(c.w[i >> 1] >> (16 * (i & 1)));
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(pair, __NV_E4M3);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        x[i] = pack2(f.x, f.y);
+    }
+}
+
+// The smallest e with peak 2^-e <= 448 = 1.75 2^8 for the bits of a finite peak >= 0 (a significand
+// above 1.75 takes the next exponent).
+__device__ __forceinline__ int exponent_of(int bits) {
     if (bits == 0) return 0;
     const int e = ((bits + 0x1FFFFF) >> 23) - 135;
     return e < kMinExp ? kMinExp : e;
 }
 
-// |x| 2^-e as an E4M3 code, rounded up when the discarded part and the 16 random bits u carry.
-// Below the smallest normal 2^-6 the sum with 2^-6 has the subnormals' spacing.
-__device__ __forceinline__ uint32_t round_e4m3(float ax, float inv_scale, uint32_t u) {
-    if (!(ax < INFINITY)) return 0x7Fu;
-    const float y = ax * inv_scale;
-    const bool small = y < 0.015625f;
-    const uint32_t b = __float_as_uint(small ? y + 0.015625f : y) + (u << 4);
-    return (b >> 20) - (small ? 968u : 960u);
+// The same for sqrt(v), from v's bits: v 4^-e <= 448^2 = 1.53125 2^17.  (No float v above 448^2 4^e has a
+// root that rounds to 448 2^e: the next one's root lies more than half a step above it.)
+__device__ __forceinline__ int root_exponent_of(int bits) {
+    if (bits < 0x00800000) return exponent_of(__float_as_int(__fsqrt_rn(__int_as_float(bits))));
+    const int e = (((bits + 0x3BFFFF) >> 23) - 143) >> 1;
+    return e < kMinExp ? kMinExp : e;
 }
 
-__device__ __forceinline__ float finite_max(float peak, float ax) { return ax < INFINITY ? fmaxf(peak, ax) : peak; }
+// y in [0, 448] and 16 random bits at [8, 24) of u8 -> the E4M3 code in the top byte's low 7 bits,
+// off by 64: 16 (bits of y + 16 u) has the 3 leading significand bits and 4 of the exponent there,
+// and the discarded part carries when it and u say so.  Below the smallest normal 2^-6 the
+// subnormals' spacing is that of y + 2^-6, whose code is one exponent too high; halving it corrects that.
+__device__ __forceinline__ uint32_t e4m3_top(float y, uint32_t u8) {
+    if (y < 0.015625f) y = fmaf(y, 0.5f, 0.0078125f);
+    return (__float_as_uint(y) << 4) + u8;
+}
+
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+// One value with the checks that e4m3_top leaves out: blocks that hold a NaN or an infinity.
+__device__ __noinline__ uint32_t e4m3_careful(float x, int e, uint32_t u8) {
+    const float ax = fabsf(x);
+    if (!(ax < INFINITY)) return 0x7Fu;
+    return ((e4m3_top(ax * pow2(-e), u8) >> 24) & 0x7Fu) ^ 0x40u;
+}
+
+// What every element of a tensor's step needs.
+struct Step {
+    float b1, b2, c1, c2, eps;            // betas, 1 - betas
+    float rate, bias, keep, gscale;       // -lr / (1 - b1^t), 1 / sqrt(1 - b2^t), 1 - lr wd
+    uint32_t step, tensor;
+    int stochastic;
+};
+
+// A lane's first element in every array of a tensor.
+template <class P, class G, bool kState8>
+struct Bases {
+    typedef typename std::conditional<kState8, uint8_t, float>::type State;
+    P* param;
+    const G* grad;
+    State *m, *v;
+    float* master;
+    uint32_t eighth;          // its place / 8
+    __device__ __forceinline__ Bases(const Tensor& t, long long at)
+        : param(static_cast<P*>(t.param) + at), grad(static_cast<const G*>(t.grad) + at),
+          m(static_cast<State*>(t.m) + at), v(static_cast<State*>(t.v) + at), master(t.master + at),
+          eighth(static_cast<uint32_t>(at >> 3)) {}
+};
+
+// A lane's share of one block: read by load(), written by update(), `at` elements behind its first.
+template <class P, class G, bool kState8, bool kMaster>
+struct Lane {
+    typedef typename std::conditional<kMaster, float, P>::type Source;
+    typedef typename std::conditional<kState8, uint8_t, float>::type State;
+    Raw8<Source> p;
+    Raw8<G> g;
+    Raw8<State> m, v;
+
+    template <bool kVec>
+    __device__ __forceinline__ void load(const Bases<P, G, kState8>& t, int at, int live) {
+        if constexpr (kMaster) load8<kVec>(p, t.master + at, live);
+        else load8<kVec>(p, t.param + at, live);
+        load8<kVec>(g, t.grad + at, live);
+        load8<kVec>(m, t.m + at, live);
+        load8<kVec>(v, t.v + at, live);
+    }
+
+    template <bool kVec>
+    __device__ __forceinline__ void update(const Bases<P, G, kState8>& t, const Step& a, const Keys& keys, int at, int live,
+                                           int& em, int& ev) const {
+        float px[8], gx[8], mx[8], vx[8], r[8];
+        to_floats(p, px);
+        to_floats(g, gx);
+        f32x2 m2[4], v2[4];          // m and v from before, times b1 and b2
+        const f32x2 b1 = pack2(a.b1, a.b1), b2 = pack2(a.b2, a.b2);
+        if constexpr (kState8) {
+            // a code has 4 significant bits and the scales are powers of two (a value is no less than 2^-109),
+            // so that code 2^e is exact, and so is the scale's product with b1
+            decode8(m, m2);
+            decode8(v, v2);
+            const float sm = pow2(em), sv = pow2(ev);
+            const f32x2 scaled_b1 = mul2(b1, pack2(sm, sm)), scale_v = pack2(sv, sv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m2[i] = mul2(m2[i], scaled_b1);
+                v2[i] = mul2(v2[i], scale_v);
+                v2[i] = mul2(mul2(v2[i], v2[i]), b2);
+            }
+        } else {
+            to_floats(m, mx);
+            to_floats(v, vx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m2[i] = mul2(pack2(mx[2 * i], mx[2 * i + 1]), b1);
+                v2[i] = mul2(pack2(vx[2 * i], vx[2 * i + 1]), b2);
+            }
+        }
+        if (a.gscale != 1.f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) gx[i] = __fmul_rn(gx[i], a.gscale);
+        }
+
+        // Moments with every product and sum rounded by itself, so that the stored states do not depend on
+        // how the compiler contracts them (a product and a sum of two f32x2 may become one fma2: the sums
+        // stay scalar).
+        const f32x2 rate = pack2(a.rate, a.rate), bias = pack2(a.bias, a.bias), eps = pack2(a.eps, a.eps);
+        const f32x2 keep = pack2(a.keep, a.keep), c1 = pack2(a.c1, a.c1), c2 = pack2(a.c2, a.c2);
+        float peak_m = 0.f, peak_v = 0.f, peak_p = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x2 gi = pack2(gx[2 * i], gx[2 * i + 1]);
+            float x[2], y[2], u[2], w[2];
+            unpack2(m2[i], x[0], x[1]);
+            unpack2(mul2(gi, c1), y[0], y[1]);
+            unpack2(v2[i], u[0], u[1]);
+            unpack2(mul2(mul2(gi, gi), c2), w[0], w[1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                mx[2 * i + j] = __fadd_rn(x[j], y[j]);
+                vx[2 * i + j] = __fadd_rn(u[j], w[j]);
+                r[2 * i + j] = sqrt_sfu(vx[2 * i + j]);
+            }
+            unpack2(mul2(pack2(mx[2 * i], mx[2 * i + 1]), rate), x[0], x[1]);
+            unpack2(fma2(pack2(r[2 * i], r[2 * i + 1]), bias, eps), y[0], y[1]);
+            unpack2(fma2(pack2(px[2 * i], px[2 * i + 1]), keep, pack2(div_sfu(x[0], y[0]), div_sfu(x[1], y[1]))),
+                    px[2 * i], px[2 * i + 1]);
+            if constexpr (kState8) {
+                peak_m = peak3(peak_m, mx[2 * i], mx[2 * i + 1]);
+                peak_v = peak3(peak_v, vx[2 * i], vx[2 * i + 1]);
+            }
+            if constexpr (sizeof(P) == 2 && !kMaster) peak_p = peak3(peak_p, px[2 * i], px[2 * i + 1]);
+        }
+
+        Raw8<P> out;
+        from_floats(out, px);
+        if constexpr (kMaster) {
+            Raw8<float> full;
+            from_floats(full, px);
+            store8<kVec>(t.master + at, full, live);
+        } else if constexpr (sizeof(P) == 2) {
+            if (a.stochastic) {
+                uint32_t w[4] = {t.eighth + at / 8, a.step, a.tensor, kTagParam};
+                philox(w, keys);
+                if (!(peak_p < INFINITY)) {       // a sum must not carry out of a NaN: no random bits there
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (!(fabsf(px[i]) < INFINITY)) w[i >> 1] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    out.w[i] = __byte_perm(__float_as_uint(px[2 * i]) + (w[i] & 0xFFFFu),
+                                           __float_as_uint(px[2 * i + 1]) + (w[i] >> 16), 0x7632);
+            }
+        }
+        store8<kVec>(t.param + at, out, live);
+
+        if constexpr (!kState8) {
+            Raw8<float> x;
+            from_floats(x, mx);
+            store8<kVec>(t.m + at, x, live);
+            from_floats(x, vx);
+            store8<kVec>(t.v + at, x, live);
+        } else {
+            int top_m = __reduce_max_sync(0xffffffffu, __float_as_int(peak_m));
+            int top_v = __reduce_max_sync(0xffffffffu, __float_as_int(peak_v));
+            const bool careful = top_m >= 0x7F800000 || top_v >= 0x7F800000;
+            if (careful) {       // the exponents are those of the finite values
+                peak_m = peak_v = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (fabsf(mx[i]) < INFINITY) peak_m = fmaxf(peak_m, fabsf(mx[i]));
+                    if (vx[i] < INFINITY) peak_v = fmaxf(peak_v, vx[i]);
+                }
+                top_m = __reduce_max_sync(0xffffffffu, __float_as_int(peak_m));
+                top_v = __reduce_max_sync(0xffffffffu, __float_as_int(peak_v));
+            }
+            // the SFU roots are off by 2^-23 at most, too little to carry a value at the peak over its code
+            const int xm = exponent_of(top_m), xr = root_exponent_of(top_v);
+            const f32x2 sm = pack2(pow2(-xm), pow2(-xm)), sr = pack2(pow2(-xr), pow2(-xr));
+            Raw8<uint8_t> cm, cv;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t w[4] = {2 * (t.eighth + at / 8) + q, a.step, a.tensor, kTagState};
+                philox(w, keys);
+                uint32_t tm[4], tv[4];
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const int j = 4 * q + i;
+                    float y[2], z[2];
+                    unpack2(mul2(pack2(mx[j], mx[j + 1]), sm), y[0], y[1]);
+                    unpack2(mul2(pack2(r[j], r[j + 1]), sr), z[0], z[1]);
+                    tm[i] = e4m3_top(fabsf(y[0]), __byte_perm(w[i], 0, 0x4104));
+                    tm[i + 1] = e4m3_top(fabsf(y[1]), __byte_perm(w[i + 1], 0, 0x4104));
+                    tv[i] = e4m3_top(z[0], __byte_perm(w[i], 0, 0x4324));
+                    tv[i + 1] = e4m3_top(z[1], __byte_perm(w[i + 1], 0, 0x4324));
+                }
+                const uint32_t sign = top_bytes(__float_as_uint(mx[4 * q]), __float_as_uint(mx[4 * q + 1]),
+                                                __float_as_uint(mx[4 * q + 2]), __float_as_uint(mx[4 * q + 3]));
+                cm.w[q] = ((top_bytes(tm[0], tm[1], tm[2], tm[3]) & 0x7F7F7F7Fu) ^ 0x40404040u) | (sign & 0x80808080u);
+                const uint32_t c = (top_bytes(tv[0], tv[1], tv[2], tv[3]) & 0x7F7F7F7Fu) ^ 0x40404040u;
+                cv.w[q] = c;
+                if ((c - 0x01010101u) & ~c & 0x80808080u) {      // a code of 0: only for a root of 0
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (vx[4 * q + i] > 0.f && (c >> (8 * i) & 0xFFu) == 0) cv.w[q] |= 1u << (8 * i);
+                }
+                if (careful) {
+                    cm.w[q] = sign & 0x80808080u;
+                    cv.w[q] = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float vi = vx[4 * q + i];
+                        cm.w[q] |= e4m3_careful(mx[4 * q + i], xm, w[i] << 8 & 0xFFFF00u) << (8 * i);
+                        const uint32_t k = e4m3_careful(vi < INFINITY ? r[4 * q + i] : NAN, xr, w[i] >> 8 & 0xFFFF00u);
+                        cv.w[q] |= (k == 0u && vi > 0.f ? 1u : k) << (8 * i);
+                    }
+                }
+            }
+            store8<kVec>(t.m + at, cm, live);
+            store8<kVec>(t.v + at, cv, live);
+            em = xm;
+            ev = xr;
+        }
+    }
+};
 
 template <class P, class G, bool kState8, bool kMaster, int kCap>
-__global__ void __launch_bounds__(kWarps * 32) dg_adamw_kernel(const __grid_constant__ Args<kCap> a) {
+__global__ void __launch_bounds__(kWarps * 32, 4) dg_adamw_kernel(const __grid_constant__ Args<kCap> a) {
     // the tensor this CTA works on
     int lo = 0, hi = a.n_tensors;
     const int cta = blockIdx.x;
@@ -196,113 +483,78 @@ __global__ void __launch_bounds__(kWarps * 32) dg_adamw_kernel(const __grid_cons
     const Tensor& t = a.t[lo];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    double lr = a.lr;
-    float step_size = a.step_size, inv_root_bc2 = a.inv_root_bc2, gscale = a.grad_scale;
-    uint32_t step = a.step;
-    if (a.grad_scale_dev) gscale *= *a.grad_scale_dev;
-    if (a.lr_dev) lr = static_cast<double>(*a.lr_dev);
+    Step s{a.b1, a.b2, a.one_minus_b1, a.one_minus_b2, a.eps, -a.step_size, a.inv_root_bc2, t.decay, a.grad_scale,
+           a.step, a.first_tensor + lo, a.stochastic};
+    if (a.grad_scale_dev) s.gscale *= *a.grad_scale_dev;
     if (a.step_dev || a.lr_dev) {
-        __shared__ double corr[2];
-        if (a.step_dev) step = static_cast<uint32_t>(*a.step_dev);
+        __shared__ float shared[3];
+        if (a.step_dev) s.step = static_cast<uint32_t>(*a.step_dev);
         if (threadIdx.x == 0) {
+            const double lr = a.lr_dev ? static_cast<double>(*a.lr_dev) : a.lr;
             // 1 - b^t without cancellation; b = 0 gives 1
-            corr[0] = a.beta1 > 0 ? -expm1(step * log(a.beta1)) : 1.0;
-            corr[1] = a.beta2 > 0 ? -expm1(step * log(a.beta2)) : 1.0;
+            const double c1 = a.beta1 > 0 ? -expm1(s.step * log(a.beta1)) : 1.0;
+            const double c2 = a.beta2 > 0 ? -expm1(s.step * log(a.beta2)) : 1.0;
+            shared[0] = static_cast<float>(-lr / c1);
+            shared[1] = static_cast<float>(1.0 / sqrt(c2));
+            shared[2] = static_cast<float>(1.0 - lr * static_cast<double>(t.decay));
         }
         __syncthreads();
-        step_size = static_cast<float>(lr / corr[0]);
-        inv_root_bc2 = static_cast<float>(1.0 / sqrt(corr[1]));
+        s.rate = shared[0];
+        s.bias = shared[1];
+        s.keep = shared[2];
     }
-    const float keep = static_cast<float>(1.0 - lr * static_cast<double>(t.weight_decay));
 
+    // This warp's blocks are consecutive, so that their addresses differ by constants.
     const long long n = t.n;
-    const long long first = static_cast<long long>(cta - a.first_cta[lo]) * a.blocks_per_warp * kWarps;
-    for (int k = 0; k < a.blocks_per_warp; ++k) {
-        // neighbouring warps on neighbouring blocks, so that a CTA's accesses are one run of memory
-        const long long blk = first + static_cast<long long>(k) * kWarps + warp;
-        const long long at = blk * kBlock + lane * 8;
-        if (blk * kBlock >= n) break;
-        const int live = at >= n ? 0 : (n - at < 8 ? static_cast<int>(n - at) : 8);
-        const bool vec = t.aligned && live == 8;
-
-        float p[8], g[8], m[8], v[8];
-        if constexpr (kMaster) load8(t.master + at, vec, live, p);
-        else load8(static_cast<const P*>(t.param) + at, vec, live, p);
-        load8(static_cast<const G*>(t.grad) + at, vec, live, g);
+    const int first_own = warp * a.blocks_per_warp;
+    const long long base = (static_cast<long long>(cta - a.first_cta[lo]) * kWarps * a.blocks_per_warp + first_own) * kBlock;
+    const int blocks = static_cast<int>(min(static_cast<long long>(a.blocks_per_warp), (n - base + kBlock - 1) / kBlock));
+    const int whole = t.aligned ? static_cast<int>(min(static_cast<long long>(blocks), (n - base) / kBlock)) : 0;
+    // A CTA's exponents are read before any is written and written together at the end: read and written one
+    // by one, each read waited for the neighbours' writes to the same 32-byte sector (1.07 ms instead of
+    // 0.43 ms for 120 million bf16 parameters).
+    __shared__ int8_t exps[2][kWarps * kMaxBlocksPerWarp];
+    const long long first_block = static_cast<long long>(cta - a.first_cta[lo]) * a.blocks_per_warp * kWarps;
+    const int k = threadIdx.x;
+    const bool mine = k < a.blocks_per_warp * kWarps && (first_block + k) * kBlock < n;
+    if constexpr (kState8) {
+        if (mine) {
+            exps[0][k] = t.m_exp[first_block + k];
+            exps[1][k] = t.v_exp[first_block + k];
+        }
+        __syncthreads();
+    }
+    const Bases<P, G, kState8> from(t, base + lane * 8);
+#pragma unroll 1
+    for (int k = 0; k < blocks; ++k) {
+        Lane<P, G, kState8, kMaster> x;
+        int em = 0, ev = 0;
         if constexpr (kState8) {
-            uint32_t cm[2], cv[2];
-            load_codes(static_cast<const uint8_t*>(t.m) + at, vec, live, cm);
-            load_codes(static_cast<const uint8_t*>(t.v) + at, vec, live, cv);
-            decode8(cm, t.m_exp[blk], m);
-            decode8(cv, t.v_exp[blk], v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], v[i]);
-        } else {
-            load8(static_cast<const float*>(t.m) + at, vec, live, m);
-            load8(static_cast<const float*>(t.v) + at, vec, live, v);
+            em = exps[0][first_own + k];
+            ev = exps[1][first_own + k];
         }
-
-        // moments with every product and sum rounded by itself, so that the stored states do not
-        // depend on how the compiler contracts them
-        float peak_m = 0.f, peak_r = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float gi = __fmul_rn(g[i], gscale);
-            m[i] = __fadd_rn(__fmul_rn(m[i], a.b1), __fmul_rn(gi, a.one_minus_b1));
-            v[i] = __fadd_rn(__fmul_rn(v[i], a.b2), __fmul_rn(__fmul_rn(gi, gi), a.one_minus_b2));
-            const float r = __fsqrt_rn(v[i]);
-            p[i] = fmaf(p[i], keep, -__fdividef(m[i] * step_size, fmaf(r, inv_root_bc2, a.eps)));
-            if constexpr (kState8) {
-                v[i] = r;
-                peak_m = finite_max(peak_m, fabsf(m[i]));
-                peak_r = finite_max(peak_r, r);
-            }
-        }
-
-        if constexpr (kMaster) {
-            store8(t.master + at, vec, live, p);
-            store8(static_cast<P*>(t.param) + at, vec, live, p);
+        if (k < whole) {
+            x.template load<true>(from, k * kBlock, 8);
+            x.template update<true>(from, s, a.keys, k * kBlock, 8, em, ev);
         } else {
-            if constexpr (sizeof(P) == 2) {
-                if (a.stochastic) {
-                    uint32_t w[4] = {static_cast<uint32_t>(at >> 3), step, a.first_tensor + lo, kTagParam};
-                    philox4x32_10(w, a.seed_lo, a.seed_hi);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t u = (w[i >> 1] >> (16 * (i & 1))) & 0xFFFFu;
-                        if (fabsf(p[i]) < INFINITY)
-                            p[i] = __uint_as_float((__float_as_uint(p[i]) + u) & 0xFFFF0000u);
-                    }
-                }
-            }
-            store8(static_cast<P*>(t.param) + at, vec, live, p);
+            const long long left = n - (base + k * kBlock + lane * 8);
+            const int live = left <= 0 ? 0 : (left < 8 ? static_cast<int>(left) : 8);
+            x.template load<false>(from, k * kBlock, live);
+            x.template update<false>(from, s, a.keys, k * kBlock, live, em, ev);
         }
         if constexpr (kState8) {
-            const int em = block_exponent(peak_m), er = block_exponent(peak_r);
-            const float sm = __int_as_float((127 - em) << 23), sr = __int_as_float((127 - er) << 23);
-            uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t w[4] = {static_cast<uint32_t>((at >> 2) + q), step, a.first_tensor + lo, kTagState};
-                philox4x32_10(w, a.seed_lo, a.seed_hi);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float mi = m[4 * q + i], ri = v[4 * q + i];
-                    const uint32_t sign = (__float_as_uint(mi) >> 31 && mi != 0.f) ? 0x80u : 0u;
-                    cm[q] |= (round_e4m3(fabsf(mi), sm, w[i] & 0xFFFFu) | sign) << (8 * i);
-                    const uint32_t c = round_e4m3(ri, sr, w[i] >> 16);
-                    cv[q] |= (c == 0u && ri > 0.f ? 1u : c) << (8 * i);
-                }
-            }
-            store_codes(static_cast<uint8_t*>(t.m) + at, vec, live, cm);
-            store_codes(static_cast<uint8_t*>(t.v) + at, vec, live, cv);
+            __syncwarp();
             if (lane == 0) {
-                t.m_exp[blk] = static_cast<int8_t>(em);
-                t.v_exp[blk] = static_cast<int8_t>(er);
+                exps[0][first_own + k] = static_cast<int8_t>(em);
+                exps[1][first_own + k] = static_cast<int8_t>(ev);
             }
-        } else {
-            store8(static_cast<float*>(t.m) + at, vec, live, m);
-            store8(static_cast<float*>(t.v) + at, vec, live, v);
+        }
+    }
+    if constexpr (kState8) {
+        __syncthreads();
+        if (mine) {
+            t.m_exp[first_block + k] = exps[0][k];
+            t.v_exp[first_block + k] = exps[1][k];
         }
     }
 }
@@ -346,8 +598,10 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
     a.lr_dev = p->lr_dev;
     a.step_dev = p->step_dev;
     a.grad_scale_dev = p->grad_scale_dev;
-    a.seed_lo = static_cast<uint32_t>(p->seed);
-    a.seed_hi = static_cast<uint32_t>(p->seed >> 32);
+    for (uint32_t r = 0; r < 10; ++r) {
+        a.keys.k[r][0] = static_cast<uint32_t>(p->seed) + r * 0x9E3779B9u;
+        a.keys.k[r][1] = static_cast<uint32_t>(p->seed >> 32) + r * 0xBB67AE85u;
+    }
     a.step = static_cast<uint32_t>(p->step);
     a.first_tensor = static_cast<uint32_t>(begin);
     a.stochastic = p->stochastic;
@@ -369,7 +623,9 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
         t.v_exp = x.v_exp;
         t.master = x.master;
         t.n = x.n;
-        t.weight_decay = x.weight_decay;
+        t.decay = p->lr_dev || p->step_dev
+                      ? x.weight_decay
+                      : static_cast<float>(1.0 - p->lr * static_cast<double>(x.weight_decay));
         t.aligned = !(misaligned(x.param, pa) || misaligned(x.grad, ga) || misaligned(x.m, sa) ||
                       misaligned(x.v, sa) || misaligned(x.master, 32));
         master = master || x.master;
@@ -445,11 +701,12 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     }
     // a master copy for all tensors of a call or for none, and only beside bf16 parameters that it rounds to
     if (with_master != 0 && (with_master != live || p->param_type != DG_BF16 || p->stochastic)) return DG_EINVAL;
-    // Few elements: one block a warp, to spread them over the SMs.  Many: 4 blocks a warp, which
-    // shares a CTA's search of the list over more work.
+    // Few elements: one block a warp, to spread them over the SMs.  Many: 8 blocks a warp, which share the
+    // search of the list and the constants (120 million bf16 parameters, 8-bit states: 0.311 ms with 8, 0.320
+    // with 4).
     const int sms = device_sm_count();
     if (sms <= 0) return DG_ECUDA;
-    const int bpw = total > static_cast<long long>(sms) * 8 * kWarps * kBlock * 4 ? 4 : 1;
+    const int bpw = total > static_cast<long long>(sms) * 8 * kWarps * kBlock * kMaxBlocksPerWarp ? kMaxBlocksPerWarp : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launches = 0;
     for (int begin = 0; begin < n_tensors;) {

@@ -63,6 +63,26 @@ def copy(S):
     return {k: None if x is None else [t.cpu().clone() for t in x] for k, x in S.items()}
 
 
+def check_roots(codes, exps, v, u):
+    """Exponents are those of the correctly rounded roots.  The roots that are rounded to codes come from the SFU,
+    off by at most 2^-23 of themselves: a code is one of those of the roots 2^-22 below and above."""
+    r = np.sqrt(v)
+    _, e = adamw.encode(r, u, root=True)
+    assert np.array_equal(exps.cpu().numpy(), e)
+    scale = 2.0 ** -np.repeat(e, 256)[:len(v)].astype(np.float64)
+    y, got = r.astype(np.float64) * scale, adamw.decode(codes.cpu().numpy(), np.zeros_like(e))
+
+    def cut(y):
+        y = np.where(y < 2.0 ** -6, (y + 2.0 ** -6).astype(np.float32) - 2.0 ** -6, y)
+        step = 2.0 ** (np.floor(np.log2(np.maximum(y, 2.0 ** -6))) - 3)
+        return np.where(r > 0, np.maximum(np.floor(y / step + u / 65536) * step, 2.0 ** -9), 0)
+
+    lo, hi = cut(y * (1 - 2.0 ** -22)), cut(np.minimum(y * (1 + 2.0 ** -22), 448))
+    fin = np.isfinite(y)
+    assert np.all(((got >= lo) & (got <= hi))[fin]) and np.isnan(got[~fin]).all()
+    assert len(v) < 1000 or np.mean(lo == hi) > 0.999
+
+
 def check(before, S, t, seed, decay, bits, stochastic, grad_scale=1.0, lr=LR):
     """What the call left in S, against the oracle's step from `before`."""
     for i, p0 in enumerate(before["p"]):
@@ -94,9 +114,8 @@ def check(before, S, t, seed, decay, bits, stochastic, grad_scale=1.0, lr=LR):
         else:
             um, uv = adamw.random_halves(seed, n, t, i)
             cm, em = adamw.encode(m, um)
-            cv, ev = adamw.encode(np.sqrt(v), uv, root=True)
-            assert np.array_equal(S["m_exp"][i].cpu().numpy(), em) and np.array_equal(S["v_exp"][i].cpu().numpy(), ev)
-            assert np.array_equal(S["m"][i].cpu().numpy(), cm) and np.array_equal(S["v"][i].cpu().numpy(), cv)
+            assert np.array_equal(S["m_exp"][i].cpu().numpy(), em) and np.array_equal(S["m"][i].cpu().numpy(), cm)
+            check_roots(S["v"][i], S["v_exp"][i], v, uv)
         got = S["p"][i].cpu()
         if before["master"] is not None:
             mast = S["master"][i].cpu()
@@ -203,10 +222,9 @@ def test_extreme_gradients(dg):
         m, v = adamw.moments(g.numpy(), np.zeros(n), np.zeros(n), B1, B2)
         um, uv = adamw.random_halves(3, n, 1, 0)
         cm, em = adamw.encode(m, um)
-        cv, ev = adamw.encode(np.sqrt(v), uv, root=True)
-    assert np.array_equal(S["m_exp"][0].cpu().numpy(), em) and np.array_equal(S["v_exp"][0].cpu().numpy(), ev)
+        check_roots(S["v"][0], S["v_exp"][0], v, uv)
+    assert np.array_equal(S["m_exp"][0].cpu().numpy(), em)
     assert np.array_equal(S["m"][0].cpu().numpy() & 0x7F, cm & 0x7F)
-    assert np.array_equal(S["v"][0].cpu().numpy(), cv)
     moved = S["p"][0].cpu().numpy()
     odd = ~np.isfinite(moved)
     assert set(np.flatnonzero(odd)) <= {600, 700} and odd[600]
