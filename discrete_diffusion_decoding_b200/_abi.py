@@ -44,6 +44,10 @@ class DgAdamWParams(ctypes.Structure):
                 ("param_type", ctypes.c_int), ("grad_type", ctypes.c_int), ("stochastic", ctypes.c_int)]
 
 
+for _s in (DgXentParams, DgAdamWParams):
+    _s.NAMES = frozenset(name for name, _ in _s._fields_)
+
+
 class DgAdamWTensor(ctypes.Structure):
     _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
                 ("v", ctypes.c_void_p), ("m_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),

@@ -10,19 +10,25 @@
 // without the cancellation of lse - z[i, y_i] and of p - 1 at positions the head is sure of.
 //
 // Launches.  dg_xent_pack_kernel gathers the hidden states of the positions that count (target not
-// ignored; backward: and dloss not 0) into a dense, zero-padded copy, so that ignored positions cost
-// nothing and cannot reach a product, whatever they hold.  The number kept stays on the device; the
-// products read it there.  Forward: one product over [positions, vocabulary] tiles whose epilogue
-// keeps a running (maximum, sum) per row and tile, and a merge.  Backward, for each piece of the
-// vocabulary: the same product again with the epilogue writing G's piece in bf16 (the operand type
-// of the two products that read it; each entry is off by at most 2^-9 of itself, as the output in
-// bf16 is), then one launch for both gradients' tiles, dW's written once and dh's added in fp32 to
-// slabs that the last launch sums, rounds and scatters.
+// ignored; backward: and dloss not 0) into a dense copy, so that ignored positions cost nothing and
+// cannot reach a product, whatever they hold.  The number kept stays on the device; the products
+// read it there.  It also takes the target's logit, as one fp32 dot product: the largest term of the
+// loss is then not subject to the tensor core's truncation.  Forward: one product over [positions,
+// vocabulary] tiles whose epilogue keeps a (maximum, sum) per row and half tile, and a merge.
+// Backward: launch k computes G for piece k + 1 of the vocabulary (the same product, G written in
+// bf16, the operand type of the two products that read it: each entry is off by at most 2^-8 of
+// itself, as an output in bf16 is) and both gradients' tiles for piece k, so that the tails, the
+// memory-bound and the compute-bound tiles of the three overlap; dW is written once, dh is added in
+// fp32 to slabs that the last launch sums, rounds and scatters.
 //
-// The products run on CTA pairs (cta_group::2 UMMA, 256 x 256 tiles, K in stages of 64): warp 0
-// loads (TMA, ring of kStages x 32 KB a CTA), warp 1 issues, warps 4-7 (one TMEM lane quarter each,
-// thread = row) run the epilogue of one accumulator while the other is computed.  Every wait is
-// bounded, and the producers leave only once the loads they issued have landed.
+// The products run on CTA pairs (cta_group::2 UMMA, 256 x 256 tiles, K in stages of 64).  An item is two
+// tiles side by side that share A: 48 KB a stage and CTA for 1024 tensor cycles, where one tile takes 32 KB for
+// 512 and the reads from L2 (about 50 bytes a cycle and SM here) hold the tensor core at 0.78.  Warp 0 loads
+// (TMA, a ring of 12 boxes), warp 1 issues, warp 2 of the pair's leader fetches items from a counter in memory
+// (longest kind first, single tiles last, so that the pairs finish together), warps 4-11 (two for each TMEM lane
+// quarter, each one half of a tile's columns, thread = row) take the two accumulators in turn to registers and
+// run the epilogue there; the next item's first stages are multiplied for the first accumulator meanwhile.
+// Every wait is bounded, and the producers leave only once the loads they issued have landed.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -42,21 +48,27 @@ namespace dg {
 namespace {
 
 constexpr int kTile = 256;                 // rows and columns of an output tile (one CTA pair)
+constexpr int kHalf = kTile / 2;           // rows of a CTA, columns of an epilogue group
 constexpr int kK = 64;                     // contraction elements per stage
-constexpr int kStages = 7;
-constexpr int kOperand = 16 * 1024;        // one operand's box per CTA and stage
-constexpr int kStageBytes = 2 * kOperand;
-constexpr int kSmem = kStages * kStageBytes + 1024;
-constexpr int kXThreads = 256;
+constexpr int kOperand = 16 * 1024;        // one 128 x 64 operand box per CTA and stage
+constexpr int kMaxStages = 6;              // a stage is A and B of one or two tiles: 2 or 3 of the ring's boxes
+constexpr int kBoxes = 12;
+constexpr int kXThreads = 384;
 constexpr int kEpiWarp0 = 4;
-constexpr int kPackRows = 16;              // rows per CTA of the gather
+constexpr int kEpiBytes = 4096;            // an epilogue warp's rows on their way out: 32 x 128 bytes
+constexpr int kSmemBytes = kBoxes * kOperand + 8 * kEpiBytes + 1024;
+constexpr int kSched = 2;                  // items in hand: the one in work and the next
+constexpr int kPackRows = 8;               // rows per CTA of the gather
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum : int {
     kErrEmpty = 401, kErrFull = 402, kErrAccFree = 403, kErrAccFull = 404, kErrDrainLoads = 405, kErrDrainMma = 406,
+    kErrSchedFree = 407, kErrSched = 408,
 };
 
-enum Mode { kModeLoss, kModeLogits, kModeGrads };
+// What a tile is of: the forward's logits, G's piece, dh, dW.
+enum Kind { kLoss, kLogits, kDh, kDw };
 
 __device__ __forceinline__ float exp2_sfu(float x) {
     float y;
@@ -75,21 +87,25 @@ struct Packed {
     int* count;
     int32_t* row;        // original position
     int32_t* target;     // target column, -1 when it lies outside the vocabulary
+    float* zt2;          // forward: the target's logit in log2 units
     float* lse2;         // backward: lse in log2 units
     float* coef;         // backward: dloss / T
     float* tcoef;        // backward: the target's entry of G
-    __nv_bfloat16* h;    // [rounded up to 256 rows, d]
+    __nv_bfloat16* h;    // [rounded up to 256 rows, d]; zeros up to a multiple of 64 rows
+    uint32_t* tickets;   // one counter of tiles for each launch of products
+    int n_tickets;
 };
 
 struct PackArgs {
     Packed out;
     const __nv_bfloat16* h;
+    const __nv_bfloat16* W;
     long long h_stride;
     const void* targets;
     int targets64;
     long long ignore;
     int n, d, vocab;
-    float inv_t;
+    float inv_t, scale_log2;
     const float* loss_in;    // backward inputs (null in the forward)
     const float* lse_in;
     const float* dloss;
@@ -107,14 +123,24 @@ __device__ __forceinline__ void zero_row(__nv_bfloat16* dst, int d, int lane) {
     for (int c = lane * 8; c < d; c += 256) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
 }
 
-// CTA b looks at rows [16 b, 16 b + 16).  Each CTA counts the kept positions before its rows (and all of them)
-// itself: N / 256 coalesced reads a thread from L2, cheaper than a scan launch before this one.
+__device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
+    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        acc = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16), acc);
+        acc = fmaf(__uint_as_float(x[i] & 0xFFFF0000u), __uint_as_float(y[i] & 0xFFFF0000u), acc);
+    }
+    return acc;
+}
+
+// CTA b looks at rows [8 b, 8 b + 8), a warp at one.  Each CTA counts the kept positions before its rows (and
+// all of them) itself: N / 256 coalesced reads a thread from L2, cheaper than a scan launch before this one.
 __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
     __shared__ int warp_before[8], warp_all[8];
-    __shared__ int slot[kPackRows];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = blockIdx.x * kPackRows;
     int before = 0, all = 0;
+#pragma unroll 4
     for (int i = tid; i < a.n; i += 256) {
         long long y;
         const int k = counts(a, i, y);
@@ -133,302 +159,367 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
         before += warp_before[w];
         all += warp_all[w];
     }
-    if (warp == 0) {
-        const int i = r0 + lane;
-        long long y = 0;
-        const bool k = lane < kPackRows && i < a.n && counts(a, i, y);
-        const uint32_t kept = __ballot_sync(0xffffffffu, k);
-        const int at = before + __popc(kept & ((1u << lane) - 1u));
-        if (lane < kPackRows) slot[lane] = k ? at : -1;
-        if (k) {
-            const bool inside = y >= 0 && y < a.vocab;
-            a.out.row[at] = i;
-            a.out.target[at] = inside ? static_cast<int32_t>(y) : -1;
-            if (a.dloss) {
-                const float c = inside ? a.dloss[i] * a.inv_t : NAN;
-                a.out.coef[at] = c;
-                a.out.tcoef[at] = c * expm1f(-a.loss_in[i]);
-                a.out.lse2[at] = a.lse_in[i] * kLog2e;
-            }
-        } else if (lane < kPackRows && i < a.n && a.loss_out) {
-            a.loss_out[i] = 0.f;
-            if (a.lse_out) a.lse_out[i] = 0.f;
-        }
-        if (blockIdx.x == 0 && lane == 0) {
+    if (blockIdx.x == 0) {
+        if (tid == 0) {
             *a.out.err = 0;
             *a.out.count = all;
         }
+        for (int i = tid; i < a.out.n_tickets; i += 256) a.out.tickets[i] = 0;
     }
-    __syncthreads();
-    const bool vec = (reinterpret_cast<uintptr_t>(a.h) & 15) == 0 && (a.h_stride & 7) == 0;
-    const int padded = (all + kTile - 1) / kTile * kTile;
-    for (int k = warp; k < kPackRows; k += 8) {
-        const int i = r0 + k;
-        if (i < a.n) {
-            const int s = slot[k];
-            const __nv_bfloat16* src = a.h + static_cast<long long>(i) * a.h_stride;
-            if (s < 0) {
-                if (a.dh) zero_row(a.dh + static_cast<long long>(i) * a.d, a.d, lane);
-            } else if (vec) {
-                __nv_bfloat16* dst = a.out.h + static_cast<long long>(s) * a.d;
-                for (int c = lane * 8; c < a.d; c += 256)
-                    *reinterpret_cast<uint4*>(dst + c) = *reinterpret_cast<const uint4*>(src + c);
-            } else {
-                __nv_bfloat16* dst = a.out.h + static_cast<long long>(s) * a.d;
-                for (int c = lane; c < a.d; c += 32) dst[c] = src[c];
-            }
+    // lanes 0..7 look at the CTA's rows; every warp does, for its own row's place
+    long long y = 0;
+    const bool k = lane < kPackRows && r0 + lane < a.n && counts(a, r0 + lane, y);
+    const uint32_t kept = __ballot_sync(0xffffffffu, k);
+    const int i = r0 + warp, at = before + __popc(kept & ((1u << warp) - 1u));
+    const bool mine = kept >> warp & 1u;
+    y = __shfl_sync(0xffffffffu, y, warp);
+    // the rows behind the last one kept, up to a whole stage of the products that sum over positions
+    if (i >= all && i < (all + kK - 1) / kK * kK) zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
+    if (i >= a.n) return;
+    if (!mine) {
+        if (lane == 0 && a.loss_out) {
+            a.loss_out[i] = 0.f;
+            if (a.lse_out) a.lse_out[i] = 0.f;
         }
-        // the rows behind the last one kept, up to a whole tile
-        if (i >= all && i < padded) zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
+        if (a.dh) zero_row(a.dh + static_cast<long long>(i) * a.d, a.d, lane);
+        return;
+    }
+    const bool inside = y >= 0 && y < a.vocab;
+    const __nv_bfloat16* src = a.h + static_cast<long long>(i) * a.h_stride;
+    __nv_bfloat16* dst = a.out.h + static_cast<long long>(at) * a.d;
+    const bool vec = (reinterpret_cast<uintptr_t>(a.h) & 15) == 0 && (a.h_stride & 7) == 0;
+    if (vec) {
+#pragma unroll 4
+        for (int c = lane * 8; c < a.d; c += 256)
+            *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(src + c));
+    } else {
+#pragma unroll 4
+        for (int c = lane; c < a.d; c += 32) dst[c] = __ldg(src + c);
+    }
+    float zt = 0.f;
+    if (!a.dloss && inside) {
+        // read back what this warp has just written: the same values, whatever h's alignment
+        __syncwarp();
+        const __nv_bfloat16* w = a.W + y * a.d;
+#pragma unroll 4
+        for (int c = lane * 8; c < a.d; c += 256)
+            zt = dot8(*reinterpret_cast<const uint4*>(dst + c), __ldg(reinterpret_cast<const uint4*>(w + c)), zt);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) zt += __shfl_xor_sync(0xffffffffu, zt, off);
+    }
+    if (lane == 0) {
+        a.out.row[at] = i;
+        a.out.target[at] = inside ? static_cast<int32_t>(y) : -1;
+        if (a.dloss) {
+            const float c = inside ? a.dloss[i] * a.inv_t : NAN;
+            a.out.coef[at] = c;
+            a.out.tcoef[at] = c * expm1f(-a.loss_in[i]);
+            a.out.lse2[at] = a.lse_in[i] * kLog2e;
+        } else {
+            a.out.zt2[at] = zt * a.scale_log2;
+        }
     }
 }
 
 // ------------------------------------------------------------------ the products
 struct GemmArgs {
-    // kModeLoss, kModeLogits: a0 = packed h, b0 = W, both K-major (boxes of 64 x 128 rows).
-    // kModeGrads: a0 = G K-major and b0 = W's piece MN-major for dh; a1 = G and b1 = packed h, both
-    // MN-major (boxes of 64 columns x 64 rows), for dW.
-    CUtensorMap a0, b0, a1, b1;
+    // operands, boxes of 64 columns x 128 rows (K-major) or x 64 rows (MN-major)
+    CUtensorMap h_k, w_k;            // packed h (n rows: those behind are zeros that nothing reads) and W, K-major: logits
+    CUtensorMap g_k, w_mn;           // G K-major, W MN-major: dh
+    CUtensorMap g_mn, h_mn;          // G and packed h, MN-major: dW
     Packed pk;
-    int vocab, d;
-    int v0, v_tiles;         // the piece's first column and its tiles of 256
-    int d_tiles;
-    float scale_log2;        // log2(e) / T
-    // kModeLoss
-    float2* part;            // [row][v_tiles] (maximum, sum relative to it) in log2 units
-    float* zt2;              // the target's logit, log2 units
-    // kModeLogits / kModeGrads
-    __nv_bfloat16* g;        // [rows][g_stride]
-    int g_stride;
-    // kModeGrads
-    float* slab;             // [splits][slab_rows][d] fp32 sums of dh
-    long long slab_stride;   // elements between slabs
-    int splits, kb_per_split;
-    int first_piece;
-    int want_dh, want_dw;
+    uint32_t* ticket;                // this launch's counter
+    int vocab, d, d_tiles;
+    float scale_log2;                // log2(e) / T
+    float2* part;                    // forward: [row][2 v_tiles] (maximum, sum relative to it), log2 units
+    // backward: G's buffers (buffer b starts at row b g_rows of the maps), the piece to compute G for and the
+    // piece whose gradients are computed (first column, tiles; 0 tiles: none), and the order of the kinds
+    int g_rows, g_write, g_read;
+    int v0_logits, tiles_logits, v0_grads, tiles_grads;
+    int slab_rows, splits, kb_per_split;
+    int order[3];
+    int wide;                        // a kind of at least so many tiles goes in twos
+    int tail;                        // but about so many of the last kind's
+    int first_piece, want_dh, want_dw;
+    __nv_bfloat16* g;                // [2][g_rows][piece]
+    int piece;
+    float* slab;                     // [splits][slab_rows][d] fp32 sums of dh
     void* dw;
     int dw_fp32, dw_accumulate;
 };
 
-// One output tile and its contraction range, in stages.
+// One or two output tiles (256 rows from m0, 256 or 512 columns from n0 of its matrices) and its contraction
+// range in stages.
 struct Item {
-    int m0, n0, kb0, kbs, split;
-    bool dw;
+    int kind, m0, n0, tiles, kb0, kbs, split;
+};
+constexpr int kItemWords = sizeof(Item) / 4;
+
+// Items of a grid of `outer` x `across` tiles: two tiles side by side each, a single one where `across` is odd,
+// and singles only in the last `singles` outer rows.
+struct Grid {
+    int outer, across, pairs_of, wide_rows;
+    __device__ __forceinline__ Grid(int outer_, int across_, int singles)
+        : outer(outer_), across(across_), pairs_of((across_ + 1) >> 1), wide_rows(max(0, outer_ - singles)) {}
+    __device__ __forceinline__ int count() const { return wide_rows * pairs_of + (outer - wide_rows) * across; }
+    // item t -> its outer row, first tile and number of tiles
+    __device__ __forceinline__ void at(int t, int& row, int& first, int& tiles) const {
+        const int wide = wide_rows * pairs_of;
+        if (t < wide) {
+            row = t / pairs_of;
+            first = (t - row * pairs_of) * 2;
+            tiles = min(2, across - first);
+        } else {
+            t -= wide;
+            row = wide_rows + t / across;
+            first = t - (t / across) * across;
+            tiles = 1;
+        }
+    }
 };
 
-template <int kMode>
-__device__ __forceinline__ int item_count(const GemmArgs& a, int m_tiles) {
-    if (kMode != kModeGrads) return m_tiles * a.v_tiles;
-    return (a.want_dh ? m_tiles * a.d_tiles * a.splits : 0) + (a.want_dw ? a.v_tiles * a.d_tiles : 0);
+// Item t of the launch.  Neighbouring items share rows of the larger operand, so that pairs at work together read
+// them from L2.  false behind the last item.
+template <bool kForward>
+__device__ __forceinline__ bool item_at(const GemmArgs& a, int t, int m_tiles, int rows, Item& it) {
+    if (t < 0) return false;
+    it.kb0 = it.split = 0;
+    const int kinds = kForward ? 1 : 3;
+#pragma unroll
+    for (int k = 0; k < kinds; ++k) {
+        it.kind = kForward ? static_cast<int>(kLoss) : a.order[k];
+        const int tail = k == kinds - 1 ? a.tail : 0;
+        if (kForward || it.kind == kLogits) {
+            // vocabulary tiles in twos, each with every tile of positions in turn; the last ones one by one
+            const int singles = m_tiles * a.tiles_logits < a.wide
+                                    ? a.tiles_logits
+                                    : min(a.tiles_logits, (tail + m_tiles - 1) / max(m_tiles, 1));
+            const int twos = (a.tiles_logits - singles) >> 1;
+            const int count = (a.tiles_logits - twos) * m_tiles;
+            if (t < count) {
+                const int c = t / m_tiles;
+                it.m0 = (t - c * m_tiles) * kTile;
+                it.tiles = c < twos ? 2 : 1;
+                it.n0 = (c < twos ? 2 * c : twos + c) * kTile;
+                it.kbs = (a.d + kK - 1) / kK;
+                return true;
+            }
+            t -= count;
+        } else {
+            const bool dw = it.kind == kDw;
+            const int outer = dw ? (a.want_dw ? a.tiles_grads : 0)
+                                 : (a.want_dh && a.tiles_grads ? m_tiles * a.splits : 0);
+            const Grid g(outer, a.d_tiles, outer * a.d_tiles < a.wide ? outer : (tail + a.d_tiles - 1) / a.d_tiles);
+            if (t < g.count()) {
+                int r, c;
+                g.at(t, r, c, it.tiles);
+                it.n0 = c * kTile;
+                if (dw) {
+                    it.m0 = r * kTile;
+                    it.kbs = (rows + kK - 1) / kK;
+                } else {
+                    it.split = r / m_tiles;
+                    it.m0 = (r - it.split * m_tiles) * kTile;
+                    it.kb0 = it.split * a.kb_per_split;
+                    it.kbs = min(a.kb_per_split, a.tiles_grads * (kTile / kK) - it.kb0);
+                }
+                return true;
+            }
+            t -= g.count();
+        }
+    }
+    return false;
 }
 
-// Neighbouring items share the larger operand's tile, so that pairs at work together read it from L2.
-template <int kMode>
-__device__ __forceinline__ Item item_at(const GemmArgs& a, int t, int m_tiles, int rows) {
-    Item it;
-    if (kMode != kModeGrads) {
-        it.m0 = (t % m_tiles) * kTile;
-        it.n0 = (t / m_tiles) * kTile;
-        it.kb0 = 0;
-        it.kbs = (a.d + kK - 1) / kK;
-        it.split = 0;
-        it.dw = false;
-        return it;
-    }
-    const int n_dh = a.want_dh ? m_tiles * a.d_tiles * a.splits : 0;
-    it.dw = t >= n_dh;
-    if (it.dw) t -= n_dh;
-    it.n0 = (t % a.d_tiles) * kTile;
-    const int r = t / a.d_tiles;
-    if (it.dw) {
-        it.m0 = r * kTile;
-        it.split = 0;
-        it.kb0 = 0;
-        it.kbs = (rows + kK - 1) / kK;
-    } else {
-        it.m0 = (r % m_tiles) * kTile;
-        it.split = r / m_tiles;
-        it.kb0 = it.split * a.kb_per_split;
-        const int all = a.v_tiles * (kTile / kK);
-        it.kbs = min(a.kb_per_split, all - it.kb0);
-    }
-    return it;
-}
-
-// 32 accumulator columns of this thread's row, by the whole warp together.
-__device__ __forceinline__ void acc_ld32(uint32_t addr, uint32_t (&r)[32]) {
+// This thread's row of half a tile, 128 accumulator columns, by the whole warp together.  All of it goes to
+// registers, so that the accumulator is free again before the epilogue begins.
+__device__ __forceinline__ void acc_ld128(uint32_t addr, uint32_t (&r)[kHalf]) {
     __syncwarp();
-    tmem_ld32(addr, r);
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 32) tmem_ld32(addr + c, *reinterpret_cast<uint32_t(*)[32]>(&r[c]));
     tmem_wait_ld();
 }
 
-__device__ __forceinline__ void epi_bar() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// This row's logits tile -> running maximum and sum over the columns other than the target.
-__device__ __forceinline__ void loss_epilogue(const GemmArgs& a, const Item& it, uint32_t acc, int i, int rows) {
-    const int tgt = i < rows ? a.pk.target[i] : -1;
-    float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32];
-        acc_ld32(acc + c0, r);
-        const int col = it.n0 + c0;
-        float z[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) z[k] = __uint_as_float(r[k]) * a.scale_log2;
-        if (col + 32 > a.vocab) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (col + k >= a.vocab) z[k] = -INFINITY;
-        }
-        const int off = tgt - col;
-        if (off >= 0 && off < 32) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (k == off) {
-                    a.zt2[i] = z[k];
-                    z[k] = -INFINITY;
-                }
-        }
-        float top = z[0];
-#pragma unroll
-        for (int k = 1; k < 32; ++k) top = fmaxf(top, z[k]);
-        const float m2 = fmaxf(m, top);
-        const float ref = m2 == -INFINITY ? 0.f : m2;     // nothing but masked columns so far
-        l *= exp2_sfu(m - ref);
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 32; k += 2) {
-            s0 += exp2_sfu(z[k] - ref);
-            s1 += exp2_sfu(z[k + 1] - ref);
-        }
-        l += s0 + s1;
-        m = m2;
-    }
-    if (i < rows)
-        a.part[static_cast<long long>(i) * a.v_tiles + it.n0 / kTile] = make_float2(m, l);
+// Barrier of one epilogue group (128 threads); whether any of them says so, the same answer for all.
+__device__ __forceinline__ bool group_any(int group, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(mine)), "r"(1 + group)
+        : "memory");
+    return any != 0;
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t (&u)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
-                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+__device__ __forceinline__ void group_bar(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
+
+// A warp's 32 rows x 128 bytes through shared memory: written by rows (thread = row), read as 4 rows of 8 lanes x
+// 16 bytes, so that an access to global memory covers whole lines (16 bytes of 32 rows a time, dh's tiles took 8
+// us and dW's 2.9).  Chunk c of row r lies at c ^ (r % 8): no bank conflicts either way.
+__device__ __forceinline__ void row_chunk(uint32_t own, int row, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + row * 128 + ((chunk ^ (row & 7)) << 4)), "r"(a),
+                 "r"(b), "r"(c), "r"(d)
                  : "memory");
 }
 
-// This row's logits tile -> its entries of G in bf16; rows and columns outside are 0.
-__device__ __forceinline__ void logits_epilogue(const GemmArgs& a, const Item& it, uint32_t acc, int i, int rows) {
+__device__ __forceinline__ uint4 line_chunk(uint32_t own, int row, int chunk) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(own + row * 128 + ((chunk ^ (row & 7)) << 4))
+                 : "memory");
+    return v;
+}
+
+// 64 bf16 columns of the warp's rows: out is the first row's first column, rows_left and cols_left what lies inside.
+__device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t* r, __nv_bfloat16* out,
+                                          long long stride, int rows_left, int cols_left) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        row_chunk(own, lane, c, bf16_pair(__uint_as_float(r[8 * c]), __uint_as_float(r[8 * c + 1])),
+                  bf16_pair(__uint_as_float(r[8 * c + 2]), __uint_as_float(r[8 * c + 3])),
+                  bf16_pair(__uint_as_float(r[8 * c + 4]), __uint_as_float(r[8 * c + 5])),
+                  bf16_pair(__uint_as_float(r[8 * c + 6]), __uint_as_float(r[8 * c + 7])));
+    __syncwarp();
+    const int c = lane & 7;
+    out += (lane >> 3) * stride + c * 8;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (4 * q + (lane >> 3) < rows_left && c * 8 < cols_left)
+            *reinterpret_cast<uint4*>(out + 4 * q * stride) = line_chunk(own, 4 * q + (lane >> 3), c);
+}
+
+// 32 fp32 columns (r[at], ...) of the warp's rows, each 4 given to put(row, first column, values).
+template <class Put>
+__device__ __forceinline__ void rows_fp32(uint32_t own, int lane, const uint32_t* r, int rows_left, int cols_left, Put put) {
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) row_chunk(own, lane, c, r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+    __syncwarp();
+    const int c = lane & 7;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const int row = 4 * q + (lane >> 3);
+        if (row < rows_left && c * 4 < cols_left) {
+            const uint4 v = line_chunk(own, row, c);
+            put(row, c * 4, make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                                        __uint_as_float(v.w)));
+        }
+    }
+}
+
+// This row's half tile of logits -> maximum and sum over the columns other than the target.
+__device__ __forceinline__ void loss_epilogue(const GemmArgs& a, int n0, uint32_t (&r)[kHalf], int i, int rows) {
+    if (i >= rows) return;
+    const int off = a.pk.target[i] - n0;
+    if (n0 + kHalf > a.vocab || (off >= 0 && off < kHalf)) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+            if (k == off || n0 + k >= a.vocab) r[k] = 0xFF800000u;      // -inf
+    }
+    float t[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) t[k] = __uint_as_float(r[k]);
+#pragma unroll
+    for (int k = 4; k < kHalf; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(r[k]));
+    const float m = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * a.scale_log2;
+    const float ref = m == -INFINITY ? 0.f : m;     // nothing but masked columns
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) s[k & 3] += exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -ref));
+    a.part[(static_cast<long long>(i) * a.tiles_logits) * 2 + n0 / kHalf] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
+}
+
+// This row's half tile of logits -> its entries of G in bf16; rows and columns outside are 0.
+__device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint32_t (&r)[kHalf], int i, int rows,
+                                                uint32_t own, int lane) {
     const bool live = i < rows;
-    const int tgt = live ? a.pk.target[i] - a.v0 : -1;
-    const float coef = live ? a.pk.coef[i] : 0.f, tcoef = live ? a.pk.tcoef[i] : 0.f;
-    const float lse2 = live ? a.pk.lse2[i] : 0.f;
-    __nv_bfloat16* out = a.g + static_cast<long long>(i) * a.g_stride + it.n0;
-    const int limit = a.vocab - a.v0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32];
-        acc_ld32(acc + c0, r);
-        const int col = it.n0 + c0;
-        float g[32];
+    const int limit = a.vocab - a.v0_logits;
+    const float coef = live ? a.pk.coef[i] : 0.f, lse2 = live ? a.pk.lse2[i] : 0.f;
+    const int off = live ? a.pk.target[i] - a.v0_logits - n0 : -1;
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-            g[k] = live ? exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -lse2)) * coef : 0.f;
-        const int off = tgt - col;
-        if (off >= 0 && off < 32) {
+    for (int k = 0; k < kHalf; ++k)
+        r[k] = __float_as_uint(exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -lse2)) * coef);
+    if (!live || n0 + kHalf > limit || (off >= 0 && off < kHalf)) {
+        const uint32_t tcoef = live ? __float_as_uint(a.pk.tcoef[i]) : 0u;
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (k == off) g[k] = tcoef;
-        }
-        if (col + 32 > limit) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                if (col + k >= limit) g[k] = 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < 32; k += 16) {
-            uint32_t u[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) u[q] = bf16_pair(g[k + 2 * q], g[k + 2 * q + 1]);
-            store32(out + c0 + k, u);
+        for (int k = 0; k < kHalf; ++k) {
+            if (k == off) r[k] = tcoef;
+            if (!live || n0 + k >= limit) r[k] = 0;
         }
     }
+    __nv_bfloat16* out = a.g + (static_cast<long long>(a.g_write) * a.g_rows + i - lane) * a.piece + n0;
+#pragma unroll
+    for (int c = 0; c < kHalf; c += 64) rows_bf16(own, lane, &r[c], out + c, a.piece, 32, 64);
 }
 
-// A dh tile: added to (first piece: stored in) the split's fp32 slab.  Each address is touched by one
-// thread of one launch at a time, so the order of the sums is that of the pieces.
-__device__ __forceinline__ void dh_epilogue(const GemmArgs& a, const Item& it, uint32_t acc, int i, int rows) {
-    float* out = a.slab + it.split * a.slab_stride + static_cast<long long>(i) * a.d + it.n0;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32];
-        acc_ld32(acc + c0, r);
-        if (i < rows) {
+// This row's half of a dh tile: added to (first piece: stored in) the split's fp32 slab.  Each address is touched
+// by one thread of one launch at a time, so the order of the sums is that of the pieces.
+__device__ __forceinline__ void dh_epilogue(const GemmArgs& a, int n0, int split, const uint32_t (&r)[kHalf], int i,
+                                            int rows, uint32_t own, int lane) {
+    float* out = a.slab + (static_cast<long long>(split) * a.slab_rows + i - lane) * a.d + n0;
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-                if (it.n0 + c0 + k >= a.d) break;
-                if (a.first_piece)
-                    *reinterpret_cast<uint4*>(out + c0 + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
-                else
-                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(out + c0 + k),
-                                 "f"(__uint_as_float(r[k])), "f"(__uint_as_float(r[k + 1])),
-                                 "f"(__uint_as_float(r[k + 2])), "f"(__uint_as_float(r[k + 3]))
-                                 : "memory");
-            }
-        }
+    for (int c = 0; c < kHalf; c += 32)
+        rows_fp32(own, lane, &r[c], rows - (i - lane), a.d - (n0 + c), [&](int row, int col, const float4& x) {
+            float* to = out + static_cast<long long>(row) * a.d + c + col;
+            if (a.first_piece)
+                *reinterpret_cast<float4*>(to) = x;
+            else
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(to), "f"(x.x), "f"(x.y), "f"(x.z),
+                             "f"(x.w)
+                             : "memory");
+        });
+}
+
+// This row's half of a dW tile, stored or added to what is there.  `empty`: no position counts, the sum is 0.
+__device__ __forceinline__ void dw_epilogue(const GemmArgs& a, int n0, uint32_t (&r)[kHalf], int v, bool empty,
+                                            uint32_t own, int lane) {
+    const long long first = static_cast<long long>(v - lane) * a.d + n0;
+    const int rows_left = a.vocab - (v - lane);
+    if (empty) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) r[k] = 0;
     }
-}
-
-// A dW tile: stored, or added to what is there.  `empty`: no position counts, the sum is 0.
-__device__ __forceinline__ void dw_epilogue(const GemmArgs& a, const Item& it, uint32_t acc, int row, bool empty) {
-    const long long v = static_cast<long long>(a.v0) + it.m0 + row;
-    const bool live = v < a.vocab;
-#pragma unroll 1
-    for (int c0 = 0; c0 < kTile; c0 += 32) {
-        uint32_t r[32];
-        acc_ld32(acc + c0, r);
-        if (!live) continue;
-        float x[32];
+    if (!a.dw_fp32 && !a.dw_accumulate) {
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = empty ? 0.f : __uint_as_float(r[k]);
-        const long long at = v * a.d + it.n0 + c0;
+        for (int c = 0; c < kHalf; c += 64)
+            rows_bf16(own, lane, &r[c], static_cast<__nv_bfloat16*>(a.dw) + first + c, a.d, rows_left, a.d - (n0 + c));
+        return;
+    }
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) {
-            if (it.n0 + c0 + k >= a.d) break;
+    for (int c = 0; c < kHalf; c += 32)
+        rows_fp32(own, lane, &r[c], rows_left, a.d - (n0 + c), [&](int row, int col, float4 x) {
+            const long long at = first + static_cast<long long>(row) * a.d + c + col;
             if (a.dw_fp32) {
-                float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at + k);
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float4 y = make_float4(x[k + 4 * q], x[k + 4 * q + 1], x[k + 4 * q + 2], x[k + 4 * q + 3]);
-                    if (a.dw_accumulate) {
-                        const float4 o = p[q];
-                        y = make_float4(y.x + o.x, y.y + o.y, y.z + o.z, y.w + o.w);
-                    }
-                    p[q] = y;
-                }
-            } else {
-                uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dw) + at + k);
+                float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
                 if (a.dw_accumulate) {
-                    const uint4 o = *p;
-                    const uint32_t u[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        x[k + 2 * q] += __uint_as_float(u[q] << 16);
-                        x[k + 2 * q + 1] += __uint_as_float(u[q] & 0xFFFF0000u);
-                    }
+                    const float4 o = *to;
+                    x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
                 }
-                *p = make_uint4(bf16_pair(x[k], x[k + 1]), bf16_pair(x[k + 2], x[k + 3]),
-                                bf16_pair(x[k + 4], x[k + 5]), bf16_pair(x[k + 6], x[k + 7]));
+                *to = x;
+            } else {
+                uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.dw) + at);
+                const uint2 o = *to;
+                *to = make_uint2(bf16_pair(x.x + __uint_as_float(o.x << 16), x.y + __uint_as_float(o.x & 0xFFFF0000u)),
+                                 bf16_pair(x.z + __uint_as_float(o.y << 16), x.w + __uint_as_float(o.y & 0xFFFF0000u)));
             }
-        }
-    }
+        });
 }
 
-template <int kMode>
+template <bool kForward>
 __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid_constant__ GemmArgs a) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    // full: the leader's, counting both CTAs' bytes; acc_full / acc_free: the two accumulators
-    __shared__ uint64_t full[kStages], empty[kStages], acc_full[2], acc_free[2], drain_bar, peer_bar;
-    __shared__ uint32_t tmem_base, peer_issued;
+    // full: the leader's, counting both CTAs' bytes; acc_full / acc_free: the two accumulators;
+    // sched_full / sched_free: the items fetched ahead (free: the leader's)
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_free[2], drain_bar, peer_bar;
+    __shared__ uint64_t sched_full[kSched], sched_free[kSched];
+    __shared__ uint32_t sched_item[kSched][kItemWords];
+    __shared__ uint32_t tmem_base, peer_issued, last_bytes[kMaxStages], peer_bytes[kMaxStages];
     __shared__ int abort_flag;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -437,13 +528,17 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     int* err = a.pk.err;
 
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&acc_full[i], 1);
-            mbar_init(&acc_free[i], 2);          // leader: the epilogues of both CTAs
+            mbar_init(&acc_free[i], 4);          // leader: two epilogue groups in each CTA
+        }
+        for (int i = 0; i < kSched; ++i) {
+            mbar_init(&sched_full[i], 1);
+            mbar_init(&sched_free[i], 7);        // leader: producers and epilogue groups of both, its issuer
         }
         mbar_init(&drain_bar, 1);
         mbar_init(&peer_bar, 1);
@@ -463,50 +558,92 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     const uint32_t tmem = tmem_base;
     const int rows = *a.pk.count;
     const int m_tiles = (rows + kTile - 1) / kTile;
-    const int items = item_count<kMode>(a, m_tiles);
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    // The n-th item of this pair (false: no more, or a wait ran out).  `release`: this role is done reading it.
+    auto fetch = [&](uint32_t n, Item& it) {
+        const uint32_t s = n % kSched;
+        if (!mbar_wait<true>(&sched_full[s], (n / kSched) & 1, &abort_flag, err, kErrSched)) return false;
+        const volatile uint32_t* w = sched_item[s];
+        it = Item{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3]),
+                  static_cast<int>(w[4]), static_cast<int>(w[5]), static_cast<int>(w[6])};
+        return it.kind >= 0;
+    };
+    auto release = [&](uint32_t n) { mbar_arrive_remote(&sched_free[n % kSched], 0); };
 
     if (warp == 0) {
         if (lane == 0) {
-            uint32_t issued = 0;
+            uint32_t issued = 0, freed = 0, sizes = 0;     // stages; boxes of each in flight, 2 bits, newest lowest
+            int head = 0, taken = 0;                       // the ring's next box, boxes in flight
             bool ok = true;
-            for (int t = pair; t < items && ok; t += pairs) {
-                const Item it = item_at<kMode>(a, t, m_tiles, rows);
-                const CUtensorMap* ma = kMode == kModeGrads && it.dw ? &a.a1 : &a.a0;
-                const CUtensorMap* mb = kMode == kModeGrads && it.dw ? &a.b1 : &a.b0;
-                const int m = it.m0 + static_cast<int>(prank) * 128, n = it.n0 + static_cast<int>(prank) * 128;
-                for (int kb = it.kb0; kb < it.kb0 + it.kbs; ++kb) {
-                    const int s = issued % kStages;
-                    if (issued >= kStages &&
-                        !mbar_wait(&empty[s], ((issued / kStages) - 1) & 1, &abort_flag, err, kErrEmpty)) {
-                        ok = false;
-                        break;
+            Item it;
+            for (uint32_t n = 0; ok && fetch(n, it); ++n) {
+                release(n);
+                const CUtensorMap *ma, *mb;
+                int m = it.m0 + static_cast<int>(prank) * kHalf, c = it.n0 + static_cast<int>(prank) * kHalf;
+                int ka = it.kb0 * kK, kb = ka;
+                const bool a_mn = !kForward && it.kind == kDw, b_mn = !kForward && it.kind != kLogits;
+                const uint32_t bytes = static_cast<uint32_t>(1 + it.tiles) * kOperand;
+                if (kForward || it.kind == kLogits) {
+                    ma = &a.h_k;
+                    mb = &a.w_k;
+                    c += kForward ? 0 : a.v0_logits;
+                } else if (it.kind == kDh) {
+                    ma = &a.g_k;
+                    mb = &a.w_mn;
+                    m += a.g_read * a.g_rows;
+                    kb += a.v0_grads;
+                } else {
+                    ma = &a.g_mn;
+                    mb = &a.h_mn;
+                    ka += a.g_read * a.g_rows;
+                }
+                for (int k = 0; k < it.kbs; ++k, ka += kK, kb += kK) {
+                    const int need = 1 + it.tiles;
+                    while (taken + need > kBoxes || issued - freed >= kMaxStages) {
+                        if (!mbar_wait(&empty[freed % kMaxStages], (freed / kMaxStages) & 1, &abort_flag, err, kErrEmpty)) {
+                            ok = false;
+                            break;
+                        }
+                        taken -= static_cast<int>(sizes >> (2 * (issued - freed - 1)) & 3u);
+                        ++freed;
                     }
-                    uint8_t* sa = ring + s * kStageBytes;
-                    uint8_t* sb = sa + kOperand;
+                    if (!ok) break;
+                    const int s = issued % kMaxStages;
+                    uint8_t* sa = ring + head * kOperand;
+                    head = head + 1 == kBoxes ? 0 : head + 1;
+                    taken += need;
+                    sizes = sizes << 2 | static_cast<uint32_t>(need);
                     ++issued;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2u * kStageBytes);
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2u * bytes);
+                    last_bytes[s] = bytes;
                     const uint32_t bar = smem_addr_in_rank(&full[s], 0);
-                    if (kMode == kModeGrads && it.dw) {
-                        tma_load_2d_pair(sa, ma, bar, m, kb * kK);
-                        tma_load_2d_pair(sa + kOperand / 2, ma, bar, m + 64, kb * kK);
+                    if (a_mn) {
+                        tma_load_2d_pair(sa, ma, bar, m, ka);
+                        tma_load_2d_pair(sa + kOperand / 2, ma, bar, m + 64, ka);
                     } else {
-                        tma_load_2d_pair(sa, ma, bar, kb * kK, m);
+                        tma_load_2d_pair(sa, ma, bar, ka, m);
                     }
-                    if (kMode == kModeGrads) {
-                        tma_load_2d_pair(sb, mb, bar, n, kb * kK);
-                        tma_load_2d_pair(sb + kOperand / 2, mb, bar, n + 64, kb * kK);
-                    } else {
-                        tma_load_2d_pair(sb, mb, bar, kb * kK, n);
+                    for (int j = 0; j < it.tiles; ++j) {
+                        const int cj = c + j * kTile;
+                        uint8_t* to = ring + head * kOperand;
+                        head = head + 1 == kBoxes ? 0 : head + 1;
+                        if (b_mn) {
+                            tma_load_2d_pair(to, mb, bar, cj, kb);
+                            tma_load_2d_pair(to + kOperand / 2, mb, bar, cj + 64, kb);
+                        } else {
+                            tma_load_2d_pair(to, mb, bar, kb, cj);
+                        }
                     }
                 }
             }
             // Leave only once every load issued into either CTA has landed.  Both CTAs issue the same
             // sequence of stages, all counted on the leader's barriers; after an abort the counts of a
-            // slot differ by at most one use (the next use of a slot waits for the other CTA's bytes of
-            // this one), which the leader settles with the bytes that will not come.
+            // barrier differ by at most one use (the next use waits for the other CTA's bytes of this
+            // one), which the leader settles with the bytes that will not come.
             if (!leader) {
                 st_shared_rank_u32(&peer_issued, 0, issued);
+                for (int s = 0; s < kMaxStages; ++s) st_shared_rank_u32(&peer_bytes[s], 0, last_bytes[s]);
                 mbar_arrive_remote(&peer_bar, 0);
             } else {
                 const uint64_t t0 = global_ns();
@@ -521,13 +658,13 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
                 };
                 if (wait(&peer_bar, 0, true)) {
                     const uint32_t theirs = peer_issued;
-                    for (uint32_t s = 0; s < kStages; ++s) {
-                        // uses of slot s: s, s + kStages, ...
-                        const uint32_t mine_n = issued > s ? (issued - s - 1) / kStages + 1 : 0;
-                        const uint32_t their_n = theirs > s ? (theirs - s - 1) / kStages + 1 : 0;
+                    for (uint32_t s = 0; s < kMaxStages; ++s) {
+                        // uses of barrier s: s, s + kMaxStages, ...
+                        const uint32_t mine_n = issued > s ? (issued - s - 1) / kMaxStages + 1 : 0;
+                        const uint32_t their_n = theirs > s ? (theirs - s - 1) / kMaxStages + 1 : 0;
                         if (mine_n == 0 && their_n == 0) continue;
-                        if (mine_n > their_n) mbar_complete_tx(&full[s], kStageBytes);
-                        if (their_n > mine_n) mbar_arrive_expect_tx(&full[s], kStageBytes);
+                        if (mine_n > their_n) mbar_complete_tx(&full[s], last_bytes[s]);
+                        if (their_n > mine_n) mbar_arrive_expect_tx(&full[s], peer_bytes[s]);
                         const uint32_t uses = mine_n > their_n ? mine_n : their_n;
                         if (!wait(&full[s], (uses - 1) & 1, false)) break;
                     }
@@ -536,38 +673,71 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
         }
     } else if (warp == 1) {
         if (lane == 0 && leader) {
-            uint32_t used = 0;
-            int n = 0;
+            uint32_t used = 0;              // stages
+            int head = 0;                   // the ring's box of stage `used`
+            uint32_t uses[2] = {0, 0};      // of the two accumulators
+            int next = 0;                   // the accumulator of the next item's first tile
             bool ok = true;
-            for (int t = pair; t < items && ok; t += pairs, ++n) {
-                const Item it = item_at<kMode>(a, t, m_tiles, rows);
-                const bool a_mn = kMode == kModeGrads && it.dw, b_mn = kMode == kModeGrads;
+            Item it;
+            for (uint32_t n = 0; ok && fetch(n, it); ++n) {
+                release(n);
+                const bool a_mn = !kForward && it.kind == kDw, b_mn = !kForward && it.kind != kLogits;
                 const uint32_t idesc = idesc_bf16_f32(kTile, kTile, a_mn, b_mn);
-                const uint32_t buf = n & 1;
-                if (n >= 2 && !mbar_wait(&acc_free[buf], ((n >> 1) - 1) & 1, &abort_flag, err, kErrAccFree)) break;
-                tc_fence_after();
-                for (int kb = 0; kb < it.kbs; ++kb) {
-                    const int s = used % kStages;
-                    if (!mbar_wait(&full[s], (used / kStages) & 1, &abort_flag, err, kErrFull)) {
-                        ok = false;
-                        break;
-                    }
-                    ++used;
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(ring + s * kStageBytes), sb = sa + kOperand;
+                // K step kk of a stage - K-major: 32 bytes along the swizzled row; MN-major: 16 rows of 128 bytes,
+                // the two 64-column atoms half an operand apart
+                auto box = [&](int k) { return smem_u32(ring + (k >= kBoxes ? k - kBoxes : k) * kOperand); };
+                // `ahead` stages behind the current one
+                auto multiply = [&](int ahead, int tile, bool accumulate) {
+                    int first = head + ahead * (1 + it.tiles);
+                    if (first >= kBoxes) first -= kBoxes;
+                    const uint32_t sa = box(first), sb = box(first + 1 + tile);
 #pragma unroll
                     for (int kk = 0; kk < kK / 16; ++kk) {
-                        // K-major: 32 bytes along the swizzled row; MN-major: 16 rows of 128 bytes, the two
-                        // 64-column atoms half an operand apart
                         const uint64_t ad = a_mn ? smem_desc(sa + kk * 2048, kOperand / 2, 1024, kSwizzle128B)
                                                  : smem_desc(sa + kk * 32, 16, 1024, kSwizzle128B);
                         const uint64_t bd = b_mn ? smem_desc(sb + kk * 2048, kOperand / 2, 1024, kSwizzle128B)
                                                  : smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B);
-                        umma_ss_pair(tmem + buf * kTile, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
+                        umma_ss_pair(tmem + (next ^ tile) * kTile, ad, bd, idesc, accumulate || kk != 0 ? 1u : 0u);
                     }
-                    umma_commit_pair(&empty[s], 0x3);
+                };
+                auto landed = [&](uint32_t stage) {
+                    if (!mbar_wait(&full[stage % kMaxStages], (stage / kMaxStages) & 1, &abort_flag, err, kErrFull))
+                        return false;
+                    tc_fence_after();
+                    return true;
+                };
+                auto acc_ready = [&](int acc) {
+                    if (uses[acc] > 0 &&
+                        !mbar_wait(&acc_free[acc], (uses[acc] - 1) & 1, &abort_flag, err, kErrAccFree))
+                        return false;
+                    ++uses[acc];
+                    tc_fence_after();
+                    return true;
+                };
+                ok = acc_ready(next);
+                // the stages in the ring for the first tile, then for the second once its accumulator is free
+                const int ahead = it.tiles == 2 ? min(kBoxes / 3, it.kbs) : 0;
+                for (int k = 0; ok && k < ahead; ++k) {
+                    ok = landed(used + k);
+                    if (ok) multiply(k, 0, k != 0);
                 }
-                if (ok) umma_commit_pair(&acc_full[buf], 0x3);
+                if (ok && it.tiles == 2) ok = acc_ready(next ^ 1);
+                for (int k = 0; ok && k < it.kbs; ++k) {
+                    if (k >= ahead) {
+                        ok = landed(used);
+                        if (!ok) break;
+                        multiply(0, 0, k != 0);
+                    }
+                    if (k == it.kbs - 1) umma_commit_pair(&acc_full[next], 0x3);
+                    if (it.tiles == 2) multiply(0, 1, k != 0);
+                    umma_commit_pair(&empty[used % kMaxStages], 0x3);
+                    ++used;
+                    head += 1 + it.tiles;
+                    if (head >= kBoxes) head -= kBoxes;
+                }
+                if (ok && it.kbs == 0) umma_commit_pair(&acc_full[next], 0x3);
+                if (ok && it.tiles == 2) umma_commit_pair(&acc_full[next ^ 1], 0x3);
+                if (it.tiles == 1) next ^= 1;
             }
             // every UMMA issued has completed before TMEM is released
             umma_commit_pair(&drain_bar, 0x1);
@@ -579,26 +749,67 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
                 }
             }
         }
+    } else if (warp == 2) {
+        if (lane == 0 && leader) {
+            // the pair's first tile is its own number, the others come from the counter
+            Item it;
+            for (uint32_t n = 0;; ++n) {
+                const uint32_t s = n % kSched;
+                if (n >= kSched &&
+                    !mbar_wait<true>(&sched_free[s], ((n / kSched) - 1) & 1, &abort_flag, err, kErrSchedFree))
+                    break;
+                const int t = n == 0 ? pair : pairs + static_cast<int>(atomicAdd(a.ticket, 1u));
+                const bool more = m_tiles + (kForward ? 0 : a.tiles_grads) > 0 && item_at<kForward>(a, t, m_tiles, rows, it);
+                if (!more) it = Item{-1, 0, 0, 0, 0, 0, 0};
+                const int words[kItemWords] = {it.kind, it.m0, it.n0, it.tiles, it.kb0, it.kbs, it.split};
+                for (uint32_t r = 0; r < 2; ++r) {
+#pragma unroll
+                    for (int k = 0; k < kItemWords; ++k)
+                        st_shared_rank_u32(&sched_item[s][k], r, static_cast<uint32_t>(words[k]));
+                    mbar_arrive_remote(&sched_full[s], r);
+                }
+                if (!more) break;
+            }
+        }
     } else if (warp >= kEpiWarp0) {
-        const int row = (warp - kEpiWarp0) * 32 + lane;
+        const int group = (warp - kEpiWarp0) >> 2;                 // which half of the columns
+        const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        int n = 0;
-        for (int t = pair; t < items; t += pairs, ++n) {
-            const Item it = item_at<kMode>(a, t, m_tiles, rows);
-            const uint32_t buf = n & 1;
-            mbar_wait(&acc_full[buf], (n >> 1) & 1, &abort_flag, err, kErrAccFull);
-            epi_bar();
-            if (abort_flag) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + lane_addr + buf * kTile;
-            const int r = it.m0 + static_cast<int>(prank) * 128 + row;
-            if (kMode == kModeLoss) loss_epilogue(a, it, acc, r, rows);
-            else if (kMode == kModeLogits) logits_epilogue(a, it, acc, r, rows);
-            else if (it.dw) dw_epilogue(a, it, acc, static_cast<int>(prank) * 128 + row, rows == 0);
-            else dh_epilogue(a, it, acc, r, rows);
-            tc_fence_before();
-            epi_bar();
-            if (tid == kEpiWarp0 * 32) mbar_arrive_remote(&acc_free[buf], 0);
+        const bool first = tid == (kEpiWarp0 + 4 * group) * 32;
+        const uint32_t own = smem_u32(ring + kBoxes * kOperand + (warp - kEpiWarp0) * kEpiBytes);
+        uint32_t uses[2] = {0, 0};
+        int next = 0;
+        bool ok = true;
+        Item it;
+        for (uint32_t n = 0; ok; ++n) {
+            // the same answer in every thread of the group, so that none waits alone at a barrier
+            if (group_any(group, !fetch(n, it))) break;
+            for (int j = 0; j < it.tiles; ++j) {
+                const int buf = next ^ j;
+                if (group_any(group, !mbar_wait(&acc_full[buf], uses[buf] & 1, &abort_flag, err, kErrAccFull))) {
+                    ok = false;
+                    break;
+                }
+                ++uses[buf];
+                tc_fence_after();
+                uint32_t r[kHalf];
+                acc_ld128(tmem + lane_addr + buf * kTile + group * kHalf, r);
+                tc_fence_before();
+                group_bar(group);
+                if (first) mbar_arrive_remote(&acc_free[buf], 0);
+                const int i = it.m0 + static_cast<int>(prank) * kHalf + row;
+                const int n0 = it.n0 + j * kTile + group * kHalf;
+                if constexpr (kForward) {
+                    loss_epilogue(a, n0, r, i, rows);
+                } else {
+                    if (it.kind == kLogits) logits_epilogue(a, n0, r, i, rows, own, lane);
+                    else if (it.kind == kDh) dh_epilogue(a, n0, it.split, r, i, rows, own, lane);
+                    else dw_epilogue(a, n0, r, a.v0_grads + i, rows == 0, own, lane);
+                }
+            }
+            // only now is another item fetched: a pair takes none that one ahead of it would have been free for
+            if (ok && first) release(n);
+            if (it.tiles == 1) next ^= 1;
         }
     }
     __syncwarp();
@@ -608,32 +819,37 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ merges
-// One warp per kept position: the tiles' (maximum, sum) -> loss and lse.
-__global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const float2* part, const float* zt2, int v_tiles,
-                                                            float* loss, float* lse) {
+__device__ __forceinline__ void merge_into(float& m, float& l, float om, float ol) {
+    const float m2 = fmaxf(m, om), ref = m2 == -INFINITY ? 0.f : m2;
+    l = l * exp2f(m - ref) + ol * exp2f(om - ref);
+    m = m2;
+}
+
+// One CTA per kept position: the half tiles' (maximum, sum) -> loss and lse.
+__global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const float2* part, int parts, float* loss,
+                                                            float* lse) {
+    __shared__ float2 of_warp[8];
     griddep_wait();
-    const int i = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int i = blockIdx.x, lane = threadIdx.x & 31;
     if (i >= *pk.count) return;
     float m = -INFINITY, l = 0.f;
-    const float2* p = part + static_cast<long long>(i) * v_tiles;
-    for (int k = lane; k < v_tiles; k += 32) {
+    const float2* p = part + static_cast<long long>(i) * parts;
+#pragma unroll 4
+    for (int k = threadIdx.x; k < parts; k += 256) {
         const float2 x = p[k];
-        const float m2 = fmaxf(m, x.x), ref = m2 == -INFINITY ? 0.f : m2;
-        l = l * exp2f(m - ref) + x.y * exp2f(x.x - ref);
-        m = m2;
+        merge_into(m, l, x.x, x.y);
     }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) {
-        const float om = __shfl_xor_sync(0xffffffffu, m, off), ol = __shfl_xor_sync(0xffffffffu, l, off);
-        const float m2 = fmaxf(m, om), ref = m2 == -INFINITY ? 0.f : m2;
-        l = l * exp2f(m - ref) + ol * exp2f(om - ref);
-        m = m2;
-    }
-    if (lane == 0) {
+    for (int off = 16; off; off >>= 1)
+        merge_into(m, l, __shfl_xor_sync(0xffffffffu, m, off), __shfl_xor_sync(0xffffffffu, l, off));
+    if (lane == 0) of_warp[threadIdx.x >> 5] = make_float2(m, l);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 8; ++w) merge_into(m, l, of_warp[w].x, of_warp[w].y);
         const int at = pk.row[i];
         float value = NAN, total = NAN;
         if (*pk.err == 0 && pk.target[i] >= 0) {
-            const float zt = zt2[i];
+            const float zt = pk.zt2[i];
             const float gap = l > 0.f || l != l ? (m - zt + log2f(l)) * kLn2 : -INFINITY;   // no other column: -inf
             value = fmaxf(gap, 0.f) + log1pf(expf(-fabsf(gap)));
             total = zt * kLn2 + value;
@@ -655,36 +871,31 @@ __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const fl
     if (bad && dw_words)
         for (long long k = first; k < n_dw_words; k += step) dw_words[k] = 0x7FFF7FFFu;     // NaN as bf16 and as fp32
     if (!dh) return;
-    const int vecs = d / 8;
+    const int vecs = d / 4;
     for (long long k = first; k < static_cast<long long>(rows) * vecs; k += step) {
-        const int i = static_cast<int>(k / vecs), c = static_cast<int>(k % vecs) * 8;
+        const int i = static_cast<int>(k / vecs), c = static_cast<int>(k % vecs) * 4;
         const float* src = slab + static_cast<long long>(i) * d + c;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
         for (int s = 0; s < splits; ++s) {
-            const float4 u = *reinterpret_cast<const float4*>(src + s * slab_stride);
-            const float4 w = *reinterpret_cast<const float4*>(src + s * slab_stride + 4);
+            const float4 u = __ldg(reinterpret_cast<const float4*>(src + s * slab_stride));
             x[0] += u.x;
             x[1] += u.y;
             x[2] += u.z;
             x[3] += u.w;
-            x[4] += w.x;
-            x[5] += w.y;
-            x[6] += w.z;
-            x[7] += w.w;
         }
-        uint4 o = make_uint4(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
-                             bf16_pair(x[6], x[7]));
-        if (bad) o = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
-        *reinterpret_cast<uint4*>(dh + static_cast<long long>(pk.row[i]) * d + c) = o;
+        uint2 o = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
+        if (bad) o = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
+        *reinterpret_cast<uint2*>(dh + static_cast<long long>(pk.row[i]) * d + c) = o;
     }
 }
 
 // ------------------------------------------------------------------ host side
 struct XentPlan {
     int rows_alloc, v_tiles, d_tiles, pairs;
-    int piece;               // columns per piece of the backward
+    int piece, pieces;       // columns per piece of the backward, and their number
     int splits, kb_per_split;
-    size_t err, row, target, lse2, coef, tcoef, zt2, h, part, g, slab, total;
+    size_t err, row, target, lse2, coef, tcoef, zt2, h, tickets, part, g, slab, total;
 };
 
 constexpr int kMaxRows = 1 << 22;
@@ -723,24 +934,29 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     q.zt2 = take(4 * n);
     q.h = take(2 * n * p->hidden);
     if (!backward) {
-        q.part = take(8 * n * q.v_tiles);
+        q.tickets = take(4);
+        q.part = take(16 * n * q.v_tiles);
     } else {
-        // G's piece in at most 64 MB, so that it is read back from L2
-        long long piece = (64LL << 20) / (2 * static_cast<long long>(q.rows_alloc > 0 ? q.rows_alloc : 1));
+        // A piece's rows of W in at most 48 MB and its two buffers of G in at most 96 MB, so that most of what
+        // a launch reads again is in L2; no more than the vocabulary, no less than 1024 columns.
+        long long piece = (400LL << 20) / (2 * static_cast<long long>(p->hidden));
+        const long long of_g = (400LL << 20) / (4 * static_cast<long long>(q.rows_alloc > 0 ? q.rows_alloc : 1));
+        if (piece > of_g) piece = of_g;
         piece = piece / kTile * kTile;
-        if (piece > 16384) piece = 16384;
-        if (piece < 2048) piece = 2048;
+        if (piece < 1024) piece = 1024;
         if (piece > static_cast<long long>(q.v_tiles) * kTile) piece = static_cast<long long>(q.v_tiles) * kTile;
         q.piece = static_cast<int>(piece);
-        // dh: enough tiles for every pair, split along the vocabulary
+        q.pieces = (p->vocab + q.piece - 1) / q.piece;
+        // dh: about two tiles for every pair, split along the vocabulary into no less than 8 stages
         const int kbs = q.piece / kK;
         const int tiles = m_tiles * q.d_tiles;
-        int splits = tiles > 0 ? (2 * q.pairs + tiles - 1) / tiles : 1;
-        if (splits > kbs / 4) splits = kbs / 4;
+        int splits = tiles > 0 ? (q.pairs + tiles - 1) / tiles : 1;
+        if (splits > kbs / 8) splits = kbs / 8;
         if (splits < 1) splits = 1;
         q.kb_per_split = (kbs + splits - 1) / splits;
         q.splits = (kbs + q.kb_per_split - 1) / q.kb_per_split;
-        q.g = take(2 * n * q.piece);
+        q.tickets = take(4 * static_cast<size_t>(q.pieces + 1));
+        q.g = take(2 * 2 * n * q.piece);
         q.slab = take(4 * n * p->hidden * q.splits);
     }
     q.total = o;
@@ -759,6 +975,9 @@ Packed packed_of(const XentPlan& q, void* ws) {
     k.count = k.err + 1;
     k.row = at<int32_t>(ws, q.row);
     k.target = at<int32_t>(ws, q.target);
+    k.zt2 = at<float>(ws, q.zt2);
+    k.tickets = at<uint32_t>(ws, q.tickets);
+    k.n_tickets = q.pieces + 1;
     k.lse2 = at<float>(ws, q.lse2);
     k.coef = at<float>(ws, q.coef);
     k.tcoef = at<float>(ws, q.tcoef);
@@ -767,11 +986,11 @@ Packed packed_of(const XentPlan& q, void* ws) {
 }
 
 // A row-major bf16 matrix with boxes of 64 columns x box_rows rows in 128-byte swizzled rows.
-bool encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint64_t stride, uint32_t box_rows) {
+bool encode_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     host::EncodeTiledFn enc = host::encode_fn();
     if (!enc) return false;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {stride * 2};
+    cuuint64_t strides[1] = {cols * 2};
     cuuint32_t box[2] = {64, box_rows};
     cuuint32_t es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
@@ -787,19 +1006,20 @@ bool gemm_attr_set() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return true;
-    for (auto k : {dg_xent_gemm_kernel<kModeLoss>, dg_xent_gemm_kernel<kModeLogits>, dg_xent_gemm_kernel<kModeGrads>})
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess) return false;
+    for (auto k : {dg_xent_gemm_kernel<true>, dg_xent_gemm_kernel<false>})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return false;
     done[dev] = true;
     return true;
 }
 
 // A kernel that waits (griddepcontrol.wait) for the one before it on the stream: set up while that one runs.
 template <class... KArgs, class... Args>
-cudaError_t launch_next(void (*kern)(KArgs...), int grid, int cluster, size_t smem, cudaStream_t s, Args&&... args) {
+cudaError_t launch_next(void (*kern)(KArgs...), int grid, int block, int cluster, size_t smem, cudaStream_t s,
+                        Args&&... args) {
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -814,10 +1034,10 @@ cudaError_t launch_next(void (*kern)(KArgs...), int grid, int cluster, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
-template <int kMode>
+template <bool kForward>
 cudaError_t launch_gemm(const GemmArgs& a, long long most_items, int pairs, cudaStream_t s) {
     const int grid = 2 * static_cast<int>(most_items < pairs ? most_items : pairs);
-    return launch_next(dg_xent_gemm_kernel<kMode>, grid, 2, kSmem, s, a);
+    return launch_next(dg_xent_gemm_kernel<kForward>, grid, kXThreads, 2, kSmemBytes, s, a);
 }
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
@@ -828,16 +1048,18 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
-dg_status launch_pack(const PackArgs& in, const XentPlan& q, cudaStream_t s) {
-    dg_xent_pack_kernel<<<q.rows_alloc / kPackRows, 256, 0, s>>>(in);
+dg_status launch_pack(const PackArgs& in, cudaStream_t s) {
+    dg_xent_pack_kernel<<<(in.n + kK - 1) / kK * kK / kPackRows, 256, 0, s>>>(in);
     return cudaGetLastError() == cudaSuccess ? DG_OK : DG_ECUDA;
 }
 
-PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const void* h, const void* targets) {
+PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const void* h, const void* W,
+                   const void* targets) {
     PackArgs a;
     std::memset(&a, 0, sizeof(a));
     a.out = packed_of(q, ws);
     a.h = static_cast<const __nv_bfloat16*>(h);
+    a.W = static_cast<const __nv_bfloat16*>(W);
     a.h_stride = p->h_stride ? p->h_stride : p->hidden;
     a.targets = targets;
     a.targets64 = p->target_type == DG_INT64;
@@ -846,6 +1068,7 @@ PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const v
     a.d = p->hidden;
     a.vocab = p->vocab;
     a.inv_t = static_cast<float>(1.0 / static_cast<double>(p->temperature));
+    a.scale_log2 = static_cast<float>(1.4426950408889634 / static_cast<double>(p->temperature));
     return a;
 }
 
@@ -856,6 +1079,8 @@ GemmArgs gemm_args(const dg_xent_params* p, const XentPlan& q, void* ws) {
     a.vocab = p->vocab;
     a.d = p->hidden;
     a.d_tiles = q.d_tiles;
+    a.wide = 2 * q.pairs;
+    a.tail = q.pairs;
     a.scale_log2 = static_cast<float>(1.4426950408889634 / static_cast<double>(p->temperature));
     return a;
 }
@@ -904,22 +1129,22 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
     if (!gemm_attr_set()) return DG_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-    PackArgs pa = pack_args(p, q, workspace_dev, h_dev, targets_dev);
+    PackArgs pa = pack_args(p, q, workspace_dev, h_dev, W_dev, targets_dev);
     pa.loss_out = loss_dev;
     pa.lse_out = lse_dev;
     GemmArgs ga = gemm_args(p, q, workspace_dev);
-    ga.v_tiles = q.v_tiles;
+    ga.ticket = ga.pk.tickets;
+    ga.tiles_logits = q.v_tiles;
     ga.part = at<float2>(workspace_dev, q.part);
-    ga.zt2 = at<float>(workspace_dev, q.zt2);
-    if (!encode_2d(&ga.a0, ga.pk.h, q.rows_alloc, p->hidden, p->hidden, 128) ||
-        !encode_2d(&ga.b0, W_dev, p->vocab, p->hidden, p->hidden, 128))
+    if (!encode_2d(&ga.h_k, ga.pk.h, p->n, p->hidden, kHalf) ||
+        !encode_2d(&ga.w_k, W_dev, p->vocab, p->hidden, kHalf))
         return DG_ECUDA;
-    const dg_status sp = launch_pack(pa, q, s);
+    const dg_status sp = launch_pack(pa, s);
     if (sp != DG_OK) return sp;
-    const long long items = static_cast<long long>(q.rows_alloc / kTile) * q.v_tiles;
-    if (launch_gemm<kModeLoss>(ga, items, q.pairs, s) != cudaSuccess) return DG_ECUDA;
-    if (launch_next(dg_xent_merge_kernel, (p->n + 7) / 8, 1, 0, s, ga.pk, static_cast<const float2*>(ga.part),
-                    static_cast<const float*>(ga.zt2), q.v_tiles, loss_dev, lse_dev) != cudaSuccess)
+    const long long tiles = static_cast<long long>(q.rows_alloc / kTile) * q.v_tiles;
+    if (launch_gemm<true>(ga, tiles, q.pairs, s) != cudaSuccess) return DG_ECUDA;
+    if (launch_next(dg_xent_merge_kernel, p->n, 256, 1, 0, s, ga.pk, static_cast<const float2*>(ga.part),
+                    2 * q.v_tiles, loss_dev, lse_dev) != cudaSuccess)
         return DG_ECUDA;
     set_last_launches(3);
     return DG_OK;
@@ -954,58 +1179,70 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     if (workspace_bytes < q.total) return DG_ENOMEM;
     if (!gemm_attr_set()) return DG_ECUDA;
 
-    PackArgs pa = pack_args(p, q, workspace_dev, h_dev, targets_dev);
+    PackArgs pa = pack_args(p, q, workspace_dev, h_dev, W_dev, targets_dev);
     pa.loss_in = loss_dev;
     pa.lse_in = lse_dev;
     pa.dloss = dloss_dev;
     pa.dh = static_cast<__nv_bfloat16*>(dh_dev);
-    GemmArgs la = gemm_args(p, q, workspace_dev);
-    la.g = at<__nv_bfloat16>(workspace_dev, q.g);
-    la.g_stride = q.piece;
-    if (!encode_2d(&la.a0, la.pk.h, q.rows_alloc, p->hidden, p->hidden, 128)) return DG_ECUDA;
-    GemmArgs ga = la;
-    ga.slab = at<float>(workspace_dev, q.slab);
-    ga.slab_stride = static_cast<long long>(q.rows_alloc) * p->hidden;
-    ga.splits = q.splits;
+    GemmArgs ga = gemm_args(p, q, workspace_dev);
+    void* g = at<void>(workspace_dev, q.g);
+    float* slab = at<float>(workspace_dev, q.slab);
+    ga.g_rows = ga.slab_rows = q.rows_alloc;
     ga.kb_per_split = q.kb_per_split;
     ga.want_dh = dh_dev != nullptr;
     ga.want_dw = dW_dev != nullptr;
+    ga.g = static_cast<__nv_bfloat16*>(g);
+    ga.piece = q.piece;
+    ga.slab = slab;
     ga.dw = dW_dev;
     ga.dw_fp32 = p->dw_type == DG_FP32;
     ga.dw_accumulate = p->dw_accumulate;
-    if (!encode_2d(&ga.a0, la.g, q.rows_alloc, q.piece, q.piece, 128) ||
-        !encode_2d(&ga.a1, la.g, q.rows_alloc, q.piece, q.piece, 64) ||
-        !encode_2d(&ga.b1, la.pk.h, q.rows_alloc, p->hidden, p->hidden, 64))
+    const uint64_t rows = q.rows_alloc, d = p->hidden;
+    if (!encode_2d(&ga.h_k, ga.pk.h, p->n, d, kHalf) || !encode_2d(&ga.h_mn, ga.pk.h, rows, d, kK) ||
+        !encode_2d(&ga.w_k, W_dev, p->vocab, d, kHalf) || !encode_2d(&ga.w_mn, W_dev, p->vocab, d, kK) ||
+        !encode_2d(&ga.g_k, g, 2 * rows, q.piece, kHalf) || !encode_2d(&ga.g_mn, g, 2 * rows, q.piece, kK))
         return DG_ECUDA;
-    const dg_status sp = launch_pack(pa, q, s);
+    // the kinds of tiles, longest contraction first
+    const int length[3] = {(p->hidden + kK - 1) / kK, q.kb_per_split, (p->n + kK - 1) / kK};
+    const int kind[3] = {kLogits, kDh, kDw};
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 2 - i; ++j)
+            if (length[order[j]] < length[order[j + 1]]) std::swap(order[j], order[j + 1]);
+    for (int i = 0; i < 3; ++i) ga.order[i] = kind[order[i]];
+
+    const dg_status sp = launch_pack(pa, s);
     if (sp != DG_OK) return sp;
-    int launches = 1;
     const int m_tiles = q.rows_alloc / kTile;
-    for (int v0 = 0; v0 < p->vocab; v0 += q.piece) {
-        const int cols = p->vocab - v0 < q.piece ? p->vocab - v0 : q.piece;
-        la.v0 = ga.v0 = v0;
-        la.v_tiles = ga.v_tiles = (cols + kTile - 1) / kTile;
-        const void* W_piece = static_cast<const __nv_bfloat16*>(W_dev) + static_cast<size_t>(v0) * p->hidden;
-        if (!encode_2d(&la.b0, W_piece, cols, p->hidden, p->hidden, 128) ||
-            !encode_2d(&ga.b0, W_piece, cols, p->hidden, p->hidden, 64))
-            return DG_ECUDA;
-        ga.first_piece = v0 == 0;
-        const long long items = static_cast<long long>(m_tiles) * la.v_tiles;
-        if (launch_gemm<kModeLogits>(la, items, q.pairs, s) != cudaSuccess) return DG_ECUDA;
-        // a short last piece may need fewer splits; those left out keep their sums
-        ga.splits = (ga.v_tiles * (kTile / kK) + q.kb_per_split - 1) / q.kb_per_split;
-        const long long grads = (ga.want_dh ? static_cast<long long>(m_tiles) * q.d_tiles * ga.splits : 0) +
-                                (ga.want_dw ? static_cast<long long>(ga.v_tiles) * q.d_tiles : 0);
-        if (launch_gemm<kModeGrads>(ga, grads, q.pairs, s) != cudaSuccess) return DG_ECUDA;
-        launches += 2;
+    auto tiles_of = [&](int piece) {
+        const int left = p->vocab - piece * q.piece;
+        return ((left < q.piece ? left : q.piece) + kTile - 1) / kTile;
+    };
+    for (int k = -1; k < q.pieces; ++k) {
+        ga.ticket = ga.pk.tickets + (k + 1);
+        ga.v0_logits = (k + 1) * q.piece;
+        ga.tiles_logits = k + 1 < q.pieces ? tiles_of(k + 1) : 0;
+        ga.v0_grads = k * q.piece;
+        ga.tiles_grads = k >= 0 ? tiles_of(k) : 0;
+        ga.g_write = (k + 1) & 1;
+        ga.g_read = k & 1;
+        ga.first_piece = k == 0;
+        // a short last piece may need fewer splits; the slabs left out keep their sums
+        ga.splits = (ga.tiles_grads * (kTile / kK) + q.kb_per_split - 1) / q.kb_per_split;
+        const long long tiles = static_cast<long long>(m_tiles) * ga.tiles_logits +
+                                (ga.want_dh ? static_cast<long long>(m_tiles) * q.d_tiles * ga.splits : 0) +
+                                (ga.want_dw ? static_cast<long long>(ga.tiles_grads) * q.d_tiles : 0);
+        if (launch_gemm<false>(ga, tiles, q.pairs, s) != cudaSuccess) return DG_ECUDA;
     }
-    const long long work = static_cast<long long>(p->n) * (p->hidden / 8);
+    const long long work = static_cast<long long>(p->n) * (p->hidden / 4);
     long long blocks = (work + 255) / 256;
     if (blocks > q.pairs * 16LL) blocks = q.pairs * 16LL;
-    if (launch_next(dg_xent_finish_kernel, static_cast<int>(blocks), 1, 0, s, ga.pk, static_cast<const float*>(ga.slab),
-                    ga.slab_stride, q.splits, p->hidden, static_cast<__nv_bfloat16*>(dh_dev),
-                    static_cast<uint32_t*>(dW_dev), static_cast<long long>(dw_bytes / 4)) != cudaSuccess)
+    if (launch_next(dg_xent_finish_kernel, static_cast<int>(blocks), 256, 1, 0, s, ga.pk,
+                    static_cast<const float*>(slab), static_cast<long long>(rows * d), q.splits, p->hidden,
+                    static_cast<__nv_bfloat16*>(dh_dev), static_cast<uint32_t*>(dW_dev),
+                    static_cast<long long>(dw_bytes / 4)) != cudaSuccess)
         return DG_ECUDA;
+    const int launches = q.pieces + 2;
     set_last_launches(launches + 1);
     return DG_OK;
 }

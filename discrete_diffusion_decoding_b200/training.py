@@ -6,7 +6,6 @@ every step runs in the library's sm_100a kernels, on the tensors' device and on 
 current stream.
 """
 
-import contextlib
 import ctypes
 
 import torch
@@ -31,33 +30,39 @@ def _tensor(fn, name, t, dtypes, shape, device):
     """Check one dense CUDA tensor of an entry point."""
     if not isinstance(t, torch.Tensor):
         _refuse(fn, f"{name} is not a tensor")
-    if t.device != device:
-        _refuse(fn, f"{name} is on {t.device}, expected {device}")
-    if t.dtype not in dtypes:
-        _refuse(fn, f"{name} is {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
-        _refuse(fn, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        _refuse(fn, f"{name} is not contiguous")
+    if t.device != device or t.dtype not in dtypes or t.shape != shape or not t.is_contiguous():
+        _refuse(fn, f"{name} is {'' if t.is_contiguous() else 'not contiguous, '}{t.dtype} {tuple(t.shape)} on {t.device}, "
+                    f"expected dense {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}")
 
 
-@contextlib.contextmanager
-def _launch(fn, device, stream):
-    """The device of the tensors made current, and the handle of the stream to launch on."""
+def _call(fn, device, stream, *args):
+    """The library's entry point `fn` on `stream`, or the device's current stream, with the device made current."""
     if device.type != "cuda":
         _refuse(fn, f"tensors are on {device}, expected a CUDA device")
-    if stream is not None and stream.device != device:
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
         _refuse(fn, f"the stream is on {stream.device}, the tensors on {device}")
     if torch.cuda.current_device() == device.index:
-        yield (stream or torch.cuda.current_stream(device)).cuda_stream
+        check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
     else:
         with torch.cuda.device(device):
-            yield (stream or torch.cuda.current_stream(device)).cuda_stream
+            check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
 
 
-def _set(p, overrides):
+_DEFAULTS = {}
+
+
+def _params(struct, init, overrides):
+    """A params struct with the library's defaults (init fills them, once a process) and the overrides."""
+    if struct not in _DEFAULTS:
+        p = struct()
+        init(ctypes.byref(p))
+        _DEFAULTS[struct] = p
+    p = struct.from_buffer_copy(_DEFAULTS[struct])
+    names = struct.NAMES
     for k, v in overrides.items():
-        if not hasattr(p, k):
+        if k not in names:
             raise KeyError(k)
         setattr(p, k, v)
     return p
@@ -69,9 +74,8 @@ def xent_params(n, vocab, hidden, **overrides):
 
     The types of targets and dW and the row stride of h are taken from the tensors of each call.
     """
-    p = DgXentParams()
-    lib().dg_xent_params_default(ctypes.byref(p), int(n), int(vocab), int(hidden))
-    return _set(p, overrides)
+    return _params(DgXentParams, lambda p: lib().dg_xent_params_default(p, 0, 1, 8),
+                   dict(overrides, n=int(n), vocab=int(vocab), hidden=int(hidden)))
 
 
 def xent_workspace_size(p, backward=True):
@@ -98,7 +102,7 @@ def _xent_inputs(fn, p, h, W, targets, ws):
     if not isinstance(h, torch.Tensor) or h.device.type != "cuda":
         _refuse(fn, "h is not a CUDA tensor")
     dev = h.device
-    if h.dtype != torch.bfloat16 or tuple(h.shape) != (p.n, p.hidden):
+    if h.dtype != torch.bfloat16 or h.shape != (p.n, p.hidden):
         _refuse(fn, f"h is {h.dtype} {tuple(h.shape)}, expected torch.bfloat16 {(p.n, p.hidden)}")
     stride = h.stride(0) if p.n > 1 else p.hidden
     if (p.hidden > 1 and h.stride(1) != 1 and p.n > 0) or stride < p.hidden:
@@ -120,9 +124,8 @@ def dg_xent_forward(p, h, W, targets, loss, lse, ws, stream=None):
     _tensor(fn, "loss", loss, (torch.float32,), (p.n,), dev)
     if lse is not None:
         _tensor(fn, "lse", lse, (torch.float32,), (p.n,), dev)
-    with _launch(fn, dev, stream) as s:
-        check(fn, lib().dg_xent_forward(ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse),
-                                        _ptr(ws.buf), ws.nbytes, s))
+    _call(fn, dev, stream, ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(ws.buf),
+          ws.nbytes)
 
 
 def dg_xent_backward(p, h, W, targets, loss, lse, dloss, dh, dW, ws, stream=None):
@@ -139,9 +142,8 @@ def dg_xent_backward(p, h, W, targets, loss, lse, dloss, dh, dW, ws, stream=None
     if dW is not None:
         _tensor(fn, "dW", dW, (torch.bfloat16, torch.float32), (p.vocab, p.hidden), dev)
         q.dw_type = _TYPES[dW.dtype]
-    with _launch(fn, dev, stream) as s:
-        check(fn, lib().dg_xent_backward(ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse),
-                                         _ptr(dloss), _ptr(dh), _ptr(dW), _ptr(ws.buf), ws.nbytes, s))
+    _call(fn, dev, stream, ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(dloss),
+          _ptr(dh), _ptr(dW), _ptr(ws.buf), ws.nbytes)
 
 
 class _HeadCrossEntropy(torch.autograd.Function):
@@ -183,23 +185,26 @@ def head_cross_entropy(h, W, targets, temperature=1.0, ignore_index=-100):
 
 
 # ------------------------------------------------------------------ AdamW
+_SCALARS = (("lr_dev", torch.float32), ("step_dev", torch.int32), ("grad_scale_dev", torch.float32))
+
+
 def adamw_params(**overrides):
     """dg_adamw_params (lr 1e-3, betas 0.9 / 0.999, eps 1e-8, step 1, rounding to nearest).
 
     lr_dev and grad_scale_dev (float32) and step_dev (int32) take one-element CUDA tensors that the kernel
     reads when it runs.  The types and state_bits are taken from the tensors of each call.
     """
-    p = DgAdamWParams()
-    lib().dg_adamw_params_default(ctypes.byref(p))
-    p.held = []           # the scalars' memory lives as long as p
-    for name, dtype in (("lr_dev", torch.float32), ("step_dev", torch.int32), ("grad_scale_dev", torch.float32)):
-        t = overrides.pop(name, None)
+    held = []
+    for name, dtype in _SCALARS:
+        t = overrides.get(name)
         if t is not None:
             if t.dtype != dtype or t.numel() != 1 or t.device.type != "cuda":
                 _refuse("adamw_params", f"{name} must be a one-element {dtype} CUDA tensor")
-            p.held.append(t)
-            setattr(p, name, t.data_ptr())
-    return _set(p, overrides)
+            held.append(t)
+            overrides[name] = t.data_ptr()
+    p = _params(DgAdamWParams, lambda p: lib().dg_adamw_params_default(p), overrides)
+    p.held = held         # the scalars' memory lives as long as p
+    return p
 
 
 class AdamWTensors:
@@ -282,8 +287,7 @@ class AdamWTensors:
 def dg_adamw_step(p, tensors, stream=None):
     """One AdamW step of every tensor of an AdamWTensors list; p from adamw_params (p.step counts from 1)."""
     p.param_type, p.grad_type, p.state_bits = tensors.param_type, tensors.grad_type, tensors.state_bits
-    with _launch("dg_adamw_step", tensors.device, stream) as s:
-        check("dg_adamw_step", lib().dg_adamw_step(ctypes.byref(p), tensors.table, tensors.n_tensors, s))
+    _call("dg_adamw_step", tensors.device, stream, ctypes.byref(p), tensors.table, tensors.n_tensors)
 
 
 class AdamW:
