@@ -122,6 +122,10 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // completed and their memory is visible; a no-op for a normally launched grid.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Let the grids that depend on this one (griddep_wait) be set up from now on; they still wait
+// for its completion.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Transaction bytes counted on a local barrier without a copy: stands in for bytes that
 // were expected but will never be sent (the drain of an aborted pass).
 __device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {

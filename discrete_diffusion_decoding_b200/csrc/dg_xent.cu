@@ -139,6 +139,8 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
     __shared__ int warp_before[8], warp_all[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r0 = blockIdx.x * kPackRows;
+    griddep_launch();
+    griddep_wait();
     int before = 0, all = 0;
 #pragma unroll 4
     for (int i = tid; i < a.n; i += 256) {
@@ -309,7 +311,7 @@ __device__ __forceinline__ bool item_at(const GemmArgs& a, int t, int m_tiles, i
             const bool dw = it.kind == kDw;
             const int outer = dw ? (a.want_dw ? a.tiles_grads : 0)
                                  : (a.want_dh && a.tiles_grads ? m_tiles * a.splits : 0);
-            const Grid g(outer, a.d_tiles, outer * a.d_tiles < a.wide ? outer : (tail + a.d_tiles - 1) / a.d_tiles);
+            const Grid g(outer, a.d_tiles, outer * a.d_tiles < (dw ? a.wide : a.wide / 2) ? outer : (tail + a.d_tiles - 1) / a.d_tiles);
             if (t < g.count()) {
                 int r, c;
                 g.at(t, r, c, it.tiles);
@@ -552,6 +554,12 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     tc_fence_before();
     cluster_sync_all();
     tc_fence_after();
+    griddep_launch();
+    if (warp == 0 && lane == 0) {
+        const CUtensorMap* maps[6] = {&a.h_k, &a.w_k, &a.g_k, &a.w_mn, &a.g_mn, &a.h_mn};
+#pragma unroll
+        for (int i = 0; i < (kForward ? 2 : 6); ++i) tma_prefetch_desc(maps[i]);
+    }
     griddep_wait();          // everything read below was written by the launches before this one
     fence_async_global();    // and some of it is read by TMA
 
@@ -560,16 +568,20 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     const int m_tiles = (rows + kTile - 1) / kTile;
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
-    // The n-th item of this pair (false: no more, or a wait ran out).  `release`: this role is done reading it.
+    const int m_tiles_or_dw = m_tiles + (kForward ? 0 : a.tiles_grads);
+    // The n-th item of this pair: the first is its own number, the others come from the counter (false: no more, or a wait ran out).  `release`: this role is done reading it.
     auto fetch = [&](uint32_t n, Item& it) {
-        const uint32_t s = n % kSched;
-        if (!mbar_wait<true>(&sched_full[s], (n / kSched) & 1, &abort_flag, err, kErrSched)) return false;
+        if (n == 0) return m_tiles_or_dw > 0 && item_at<kForward>(a, pair, m_tiles, rows, it);
+        const uint32_t s = (n - 1) % kSched;
+        if (!mbar_wait<true>(&sched_full[s], ((n - 1) / kSched) & 1, &abort_flag, err, kErrSched)) return false;
         const volatile uint32_t* w = sched_item[s];
         it = Item{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3]),
                   static_cast<int>(w[4]), static_cast<int>(w[5]), static_cast<int>(w[6])};
         return it.kind >= 0;
     };
-    auto release = [&](uint32_t n) { mbar_arrive_remote(&sched_free[n % kSched], 0); };
+    auto release = [&](uint32_t n) {
+        if (n > 0) mbar_arrive_remote(&sched_free[(n - 1) % kSched], 0);
+    };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -751,24 +763,22 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
         }
     } else if (warp == 2) {
         if (lane == 0 && leader) {
-            // the pair's first tile is its own number, the others come from the counter
             Item it;
-            for (uint32_t n = 0;; ++n) {
-                const uint32_t s = n % kSched;
-                if (n >= kSched &&
-                    !mbar_wait<true>(&sched_free[s], ((n / kSched) - 1) & 1, &abort_flag, err, kErrSchedFree))
+            bool more = fetch(0, it);
+            for (uint32_t k = 0; more; ++k) {       // item k + 1
+                const uint32_t s = k % kSched;
+                if (k >= kSched &&
+                    !mbar_wait<true>(&sched_free[s], ((k / kSched) - 1) & 1, &abort_flag, err, kErrSchedFree))
                     break;
-                const int t = n == 0 ? pair : pairs + static_cast<int>(atomicAdd(a.ticket, 1u));
-                const bool more = m_tiles + (kForward ? 0 : a.tiles_grads) > 0 && item_at<kForward>(a, t, m_tiles, rows, it);
+                more = item_at<kForward>(a, pairs + static_cast<int>(atomicAdd(a.ticket, 1u)), m_tiles, rows, it);
                 if (!more) it = Item{-1, 0, 0, 0, 0, 0, 0};
                 const int words[kItemWords] = {it.kind, it.m0, it.n0, it.tiles, it.kb0, it.kbs, it.split};
                 for (uint32_t r = 0; r < 2; ++r) {
 #pragma unroll
-                    for (int k = 0; k < kItemWords; ++k)
-                        st_shared_rank_u32(&sched_item[s][k], r, static_cast<uint32_t>(words[k]));
+                    for (int w = 0; w < kItemWords; ++w)
+                        st_shared_rank_u32(&sched_item[s][w], r, static_cast<uint32_t>(words[w]));
                     mbar_arrive_remote(&sched_full[s], r);
                 }
-                if (!more) break;
             }
         }
     } else if (warp >= kEpiWarp0) {
@@ -784,6 +794,7 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
         for (uint32_t n = 0; ok; ++n) {
             // the same answer in every thread of the group, so that none waits alone at a barrier
             if (group_any(group, !fetch(n, it))) break;
+            if (first) release(n);
             for (int j = 0; j < it.tiles; ++j) {
                 const int buf = next ^ j;
                 if (group_any(group, !mbar_wait(&acc_full[buf], uses[buf] & 1, &abort_flag, err, kErrAccFull))) {
@@ -807,8 +818,6 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
                     else dw_epilogue(a, n0, r, a.v0_grads + i, rows == 0, own, lane);
                 }
             }
-            // only now is another item fetched: a pair takes none that one ahead of it would have been free for
-            if (ok && first) release(n);
             if (it.tiles == 1) next ^= 1;
         }
     }
@@ -829,6 +838,7 @@ __device__ __forceinline__ void merge_into(float& m, float& l, float om, float o
 __global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const float2* part, int parts, float* loss,
                                                             float* lse) {
     __shared__ float2 of_warp[8];
+    griddep_launch();
     griddep_wait();
     const int i = blockIdx.x, lane = threadIdx.x & 31;
     if (i >= *pk.count) return;
@@ -863,6 +873,7 @@ __global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const flo
 __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const float* slab, long long slab_stride,
                                                              int splits, int d, __nv_bfloat16* dh, uint32_t* dw_words,
                                                              long long n_dw_words) {
+    griddep_launch();
     griddep_wait();
     const bool bad = *pk.err != 0;
     const int rows = *pk.count;
@@ -947,10 +958,10 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
         if (piece > static_cast<long long>(q.v_tiles) * kTile) piece = static_cast<long long>(q.v_tiles) * kTile;
         q.piece = static_cast<int>(piece);
         q.pieces = (p->vocab + q.piece - 1) / q.piece;
-        // dh: about two tiles for every pair, split along the vocabulary into no less than 8 stages
+        // dh: about one item (two tiles) for every pair, split along the vocabulary into no less than 8 stages
         const int kbs = q.piece / kK;
-        const int tiles = m_tiles * q.d_tiles;
-        int splits = tiles > 0 ? (q.pairs + tiles - 1) / tiles : 1;
+        const int items = m_tiles * ((q.d_tiles + 1) / 2);
+        int splits = items > 0 ? q.pairs / items : 1;
         if (splits > kbs / 8) splits = kbs / 8;
         if (splits < 1) splits = 1;
         q.kb_per_split = (kbs + splits - 1) / splits;
@@ -1049,8 +1060,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 dg_status launch_pack(const PackArgs& in, cudaStream_t s) {
-    dg_xent_pack_kernel<<<(in.n + kK - 1) / kK * kK / kPackRows, 256, 0, s>>>(in);
-    return cudaGetLastError() == cudaSuccess ? DG_OK : DG_ECUDA;
+    const int rows = (in.n + kK - 1) / kK * kK;
+    return launch_next(dg_xent_pack_kernel, rows / kPackRows, 256, 1, 0, s, in) == cudaSuccess ? DG_OK : DG_ECUDA;
 }
 
 PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const void* h, const void* W,
