@@ -377,8 +377,10 @@ __device__ __forceinline__ uint4 line_chunk(uint32_t own, int row, int chunk) {
 }
 
 // 64 bf16 columns of the warp's rows: out is the first row's first column, rows_left and cols_left what lies inside.
+// `value` takes the place of this thread's column `at` where that is one of the 64.
 __device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t* r, __nv_bfloat16* out,
-                                          long long stride, int rows_left, int cols_left) {
+                                          long long stride, int rows_left, int cols_left, int at = -1,
+                                          float value = 0.f) {
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 8; ++c)
@@ -386,6 +388,10 @@ __device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t
                   bf16_pair(__uint_as_float(r[8 * c + 2]), __uint_as_float(r[8 * c + 3])),
                   bf16_pair(__uint_as_float(r[8 * c + 4]), __uint_as_float(r[8 * c + 5])),
                   bf16_pair(__uint_as_float(r[8 * c + 6]), __uint_as_float(r[8 * c + 7])));
+    if (at >= 0 && at < 64)
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(own + lane * 128 + (((at >> 3) ^ (lane & 7)) << 4) + (at & 7) * 2),
+                     "h"(static_cast<unsigned short>(bf16_pair(value, 0.f)))
+                     : "memory");
     __syncwarp();
     const int c = lane & 7;
     out += (lane >> 3) * stride + c * 8;
@@ -446,17 +452,15 @@ __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint3
 #pragma unroll
     for (int k = 0; k < kHalf; ++k)
         r[k] = __float_as_uint(exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -lse2)) * coef);
-    if (!live || n0 + kHalf > limit || (off >= 0 && off < kHalf)) {
-        const uint32_t tcoef = live ? __float_as_uint(a.pk.tcoef[i]) : 0u;
+    if (!live || n0 + kHalf > limit) {
 #pragma unroll
-        for (int k = 0; k < kHalf; ++k) {
-            if (k == off) r[k] = tcoef;
+        for (int k = 0; k < kHalf; ++k)
             if (!live || n0 + k >= limit) r[k] = 0;
-        }
     }
+    const float tcoef = off >= 0 && off < kHalf ? a.pk.tcoef[i] : 0.f;
     __nv_bfloat16* out = a.g + (static_cast<long long>(a.g_write) * a.g_rows + i - lane) * a.piece + n0;
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 64) rows_bf16(own, lane, &r[c], out + c, a.piece, 32, 64);
+    for (int c = 0; c < kHalf; c += 64) rows_bf16(own, lane, &r[c], out + c, a.piece, 32, 64, off - c, tcoef);
 }
 
 // This row's half of a dh tile: added to (first piece: stored in) the split's fp32 slab.  Each address is touched

@@ -13,6 +13,9 @@ import torch
 from . import _abi
 from ._abi import DgAdamWParams, DgAdamWTensor, DgError, DgXentParams, check, lib
 
+# the handle of a device's current stream (torch.cuda.current_stream builds an object around it: 2 us)
+_current_stream = torch._C._cuda_getCurrentRawStream
+
 _TYPES = {torch.float32: _abi.DG_FP32, torch.bfloat16: _abi.DG_BF16}
 _INDEX = {torch.int32: _abi.DG_INT32, torch.int64: _abi.DG_INT64}
 BLOCK = 256       # elements of an 8-bit state that share an exponent
@@ -40,14 +43,16 @@ def _call(fn, device, stream, *args):
     if device.type != "cuda":
         _refuse(fn, f"tensors are on {device}, expected a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        handle = _current_stream(device.index)
     elif stream.device != device:
         _refuse(fn, f"the stream is on {stream.device}, the tensors on {device}")
+    else:
+        handle = stream.cuda_stream
     if torch.cuda.current_device() == device.index:
-        check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+        check(fn, getattr(lib(), fn)(*args, handle))
     else:
         with torch.cuda.device(device):
-            check(fn, getattr(lib(), fn)(*args, stream.cuda_stream))
+            check(fn, getattr(lib(), fn)(*args, handle))
 
 
 _DEFAULTS = {}
