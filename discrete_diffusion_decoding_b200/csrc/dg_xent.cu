@@ -831,6 +831,197 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     if (warp == 1) tmem_dealloc_pair(tmem, 2 * kTile);
 }
 
+// ------------------------------------------------------------------ few positions
+// The forward's product where at most 32 positions can count: the vocabulary is the rows of the tile (128 a CTA)
+// and the positions its 16 or 32 columns, so that the tensor core does not multiply 256 rows for one.  That costs
+// power, and with it the clock that the reads from memory need.  Each CTA streams its rows of W through a ring of
+// its own and each epilogue thread keeps a running (maximum, sum) of every position over the vocabulary rows it
+// sees.  At V = 262144, d = 2816, heads in turn: 243 us for 1 position (6.1 TB/s; the kernel above 342), 246 for
+// 16 (323), 265 to 280 for 32 (332).  With 64 columns the final sums over the lanes cost more than is saved on
+// smaller heads (n = 64, V = 5000: 47 us against 36; n = 33, V = 50000, d = 1000: 53 against 46).
+constexpr int kFewRows = 32;               // positions at most
+constexpr int kFewStages = 12;
+constexpr int kFewRingBytes = 220 * 1024;
+constexpr int kFewSmemBytes = kFewRingBytes + 1024;
+constexpr int kFewThreads = 256;
+
+struct FewArgs {
+    CUtensorMap h, w;        // boxes of 64 columns x columns / 128 rows, K-major
+    Packed pk;
+    int vocab, d, columns;   // columns of a tile: 16 or 32
+    float scale_log2;
+    float2* part;            // [position][4 gridDim.x]
+};
+
+template <int kColumns>
+__device__ __forceinline__ void few_epilogue(const FewArgs& a, uint32_t tmem, uint64_t* acc_full, uint64_t* acc_free,
+                                             const int* target, int* abort_flag, int rows, int tiles) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
+    float m[kColumns], l[kColumns];
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) {
+        m[c] = -INFINITY;
+        l[c] = 0.f;
+    }
+    int n = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
+        const int buf = n & 1;
+        if (group_any(0, !mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, a.pk.err, kErrAccFull))) return;
+        tc_fence_after();
+        uint32_t r[kColumns];
+#pragma unroll
+        for (int c = 0; c < kColumns; c += 16)
+            tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * kFewRows + c,
+                      *reinterpret_cast<uint32_t(*)[16]>(&r[c]));
+        tmem_wait_ld();
+        tc_fence_before();
+        group_bar(0);
+        if (row == 0) mbar_arrive(&acc_free[buf]);
+        const int v = t * kHalf + row;
+        if (v >= a.vocab) continue;
+#pragma unroll
+        for (int c = 0; c < kColumns; ++c) {
+            const float z = v == target[c] ? -INFINITY : __uint_as_float(r[c]) * a.scale_log2;
+            const float m2 = fmaxf(m[c], z), ref = m2 == -INFINITY ? 0.f : m2;
+            l[c] = l[c] * exp2_sfu(m[c] - ref) + exp2_sfu(z - ref);
+            m[c] = m2;
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < kColumns; ++c) {
+#pragma unroll
+        for (int off = 16; off; off >>= 1) {
+            const float om = __shfl_xor_sync(0xffffffffu, m[c], off), ol = __shfl_xor_sync(0xffffffffu, l[c], off);
+            const float m2 = fmaxf(m[c], om), ref = m2 == -INFINITY ? 0.f : m2;
+            l[c] = l[c] * exp2_sfu(m[c] - ref) + ol * exp2_sfu(om - ref);
+            m[c] = m2;
+        }
+        if (lane == 0 && c < rows)
+            a.part[(static_cast<long long>(c) * gridDim.x + blockIdx.x) * 4 + (warp & 3)] = make_float2(m[c], l[c]);
+    }
+}
+
+// Launched in clusters of two for the waits' abort flags; the two CTAs share nothing else.
+__global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __grid_constant__ FewArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[kFewStages], empty[kFewStages], acc_full[2], acc_free[2], drain_bar;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ int target[kFewRows];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int* err = a.pk.err;
+    if (tid == 0) {
+        for (int i = 0; i < kFewStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_free[i], 1);
+        }
+        mbar_init(&drain_bar, 1);
+        fence_mbar_init_cluster();
+        abort_flag = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, 2 * kFewRows);
+        tmem_relinquish();
+    }
+    griddep_launch();
+    if (tid == 0) {
+        tma_prefetch_desc(&a.h);
+        tma_prefetch_desc(&a.w);
+    }
+    griddep_wait();
+    const int rows = *a.pk.count;
+    if (tid < kFewRows) target[tid] = tid < rows ? a.pk.target[tid] : -1;
+    fence_async_global();
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    const int tiles = rows > 0 ? (a.vocab + kHalf - 1) / kHalf : 0;
+    const int kbs = (a.d + kK - 1) / kK;
+    const int stage_bytes = kOperand + a.columns * 128;
+    const int stages = min(kFewStages, kFewRingBytes / stage_bytes);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t once = l2_policy_evict_first();
+            uint32_t issued = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+                for (int k = 0; k < kbs; ++k) {
+                    const uint32_t s = issued % stages;
+                    if (issued >= static_cast<uint32_t>(stages) &&
+                        !mbar_wait(&empty[s], ((issued / stages) - 1) & 1, &abort_flag, err, kErrEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    ++issued;
+                    uint8_t* to = ring + s * stage_bytes;
+                    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(stage_bytes));
+                    tma_load_2d_hint(to, &a.w, &full[s], k * kK, t * kHalf, once);
+                    tma_load_2d(to + kOperand, &a.h, &full[s], k * kK, 0);
+                }
+            }
+            // leave only once every load issued has landed
+            const uint64_t t0 = global_ns();
+            for (uint32_t s = 0; s < static_cast<uint32_t>(stages); ++s) {
+                const uint32_t uses = issued > s ? (issued - s - 1) / stages + 1 : 0;
+                while (uses > 0 && !mbar_try_wait(smem_u32(&full[s]), (uses - 1) & 1))
+                    if (global_ns() - t0 > DG_WAIT_LIMIT_NS) {
+                        atomicCAS(err, 0, kErrDrainLoads);
+                        break;
+                    }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_bf16_f32(kHalf, a.columns, false, false);
+            uint32_t used = 0;
+            int n = 0;
+            bool ok = true;
+            for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
+                const int buf = n & 1;
+                if (n >= 2 && !mbar_wait(&acc_free[buf], ((n >> 1) - 1) & 1, &abort_flag, err, kErrAccFree)) break;
+                tc_fence_after();
+                for (int k = 0; k < kbs; ++k, ++used) {
+                    const uint32_t s = used % stages;
+                    if (!mbar_wait(&full[s], (used / stages) & 1, &abort_flag, err, kErrFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + s * stage_bytes), sb = sa + kOperand;
+#pragma unroll
+                    for (int kk = 0; kk < kK / 16; ++kk)
+                        umma_ss(tmem + buf * kFewRows, smem_desc(sa + kk * 32, 16, 1024, kSwizzle128B),
+                                smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B), idesc, (k | kk) != 0 ? 1u : 0u);
+                    umma_commit(&empty[s]);
+                }
+                if (ok) umma_commit(&acc_full[buf]);
+            }
+            umma_commit(&drain_bar);
+            const uint64_t t0 = global_ns();
+            while (!mbar_try_wait(smem_u32(&drain_bar), 0)) {
+                if (global_ns() - t0 > DG_WAIT_LIMIT_NS) {
+                    atomicCAS(err, 0, kErrDrainMma);
+                    break;
+                }
+            }
+        }
+    } else if (warp >= 4) {
+        if (a.columns == 16) few_epilogue<16>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles);
+        else few_epilogue<32>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles);
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 1) tmem_dealloc(tmem, 2 * kFewRows);
+}
+
 // ------------------------------------------------------------------ merges
 __device__ __forceinline__ void merge_into(float& m, float& l, float om, float ol) {
     const float m2 = fmaxf(m, om), ref = m2 == -INFINITY ? 0.f : m2;
@@ -950,7 +1141,9 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     q.h = take(2 * n * p->hidden);
     if (!backward) {
         q.tickets = take(4);
-        q.part = take(16 * n * q.v_tiles);
+        // (maximum, sum) of every half tile, or of every epilogue warp of the kernel for few positions
+        const size_t of_few = p->n <= kFewRows ? sizeof(float2) * 8 * q.pairs * kFewRows : 0;
+        q.part = take(16 * n * q.v_tiles > of_few ? 16 * n * q.v_tiles : of_few);
     } else {
         // A piece's rows of W in at most 48 MB and its two buffers of G in at most 96 MB, so that most of what
         // a launch reads again is in L2; no more than the vocabulary, no less than 1024 columns.
@@ -1021,6 +1214,8 @@ bool gemm_attr_set() {
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return true;
+    if (cudaFuncSetAttribute(dg_xent_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmemBytes) != cudaSuccess)
+        return false;
     for (auto k : {dg_xent_gemm_kernel<true>, dg_xent_gemm_kernel<false>})
         if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess) return false;
     done[dev] = true;
@@ -1147,19 +1342,41 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
     PackArgs pa = pack_args(p, q, workspace_dev, h_dev, W_dev, targets_dev);
     pa.loss_out = loss_dev;
     pa.lse_out = lse_dev;
-    GemmArgs ga = gemm_args(p, q, workspace_dev);
-    ga.ticket = ga.pk.tickets;
-    ga.tiles_logits = q.v_tiles;
-    ga.part = at<float2>(workspace_dev, q.part);
-    if (!encode_2d(&ga.h_k, ga.pk.h, p->n, p->hidden, kHalf) ||
-        !encode_2d(&ga.w_k, W_dev, p->vocab, p->hidden, kHalf))
-        return DG_ECUDA;
+    const Packed pk = pa.out;
+    float2* part = at<float2>(workspace_dev, q.part);
+    GemmArgs ga;
+    FewArgs fa;
+    int parts, grid = 0;
+    const bool few = p->n <= kFewRows;
+    if (few) {
+        std::memset(&fa, 0, sizeof(fa));
+        fa.pk = pk;
+        fa.vocab = p->vocab;
+        fa.d = p->hidden;
+        fa.columns = p->n <= 16 ? 16 : kFewRows;
+        fa.scale_log2 = pa.scale_log2;
+        fa.part = part;
+        grid = 2 * static_cast<int>(q.v_tiles < q.pairs ? q.v_tiles : q.pairs);
+        parts = 4 * grid;
+        if (!encode_2d(&fa.h, pk.h, p->n, p->hidden, fa.columns) || !encode_2d(&fa.w, W_dev, p->vocab, p->hidden, kHalf))
+            return DG_ECUDA;
+    } else {
+        ga = gemm_args(p, q, workspace_dev);
+        ga.ticket = pk.tickets;
+        ga.tiles_logits = q.v_tiles;
+        ga.part = part;
+        parts = 2 * q.v_tiles;
+        if (!encode_2d(&ga.h_k, pk.h, p->n, p->hidden, kHalf) || !encode_2d(&ga.w_k, W_dev, p->vocab, p->hidden, kHalf))
+            return DG_ECUDA;
+    }
     const dg_status sp = launch_pack(pa, s);
     if (sp != DG_OK) return sp;
     const long long tiles = static_cast<long long>(q.rows_alloc / kTile) * q.v_tiles;
-    if (launch_gemm<true>(ga, tiles, q.pairs, s) != cudaSuccess) return DG_ECUDA;
-    if (launch_next(dg_xent_merge_kernel, p->n, 256, 1, 0, s, ga.pk, static_cast<const float2*>(ga.part),
-                    2 * q.v_tiles, loss_dev, lse_dev) != cudaSuccess)
+    const cudaError_t e = few ? launch_next(dg_xent_few_kernel, grid, kFewThreads, 2, kFewSmemBytes, s, fa)
+                              : launch_gemm<true>(ga, tiles, q.pairs, s);
+    if (e != cudaSuccess) return DG_ECUDA;
+    if (launch_next(dg_xent_merge_kernel, p->n, 256, 1, 0, s, pk, static_cast<const float2*>(part), parts, loss_dev,
+                    lse_dev) != cudaSuccess)
         return DG_ECUDA;
     set_last_launches(3);
     return DG_OK;

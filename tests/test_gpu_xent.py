@@ -73,6 +73,10 @@ def check(h, W, y, dl, T, got, dw_eps=2.0 ** -8):
     (1, 1, 8, 0.0, 1.0, torch.int32),
     (1, 7, 8, 0.0, 0.5, torch.int64),
     (3, 256, 64, 0.0, 1.0, torch.int32),
+    (16, 40000, 72, 0.3, 1.0, torch.int64),
+    (17, 129, 1000, 0.0, 0.7, torch.int32),
+    (32, 38000, 64, 0.1, 1.0, torch.int32),
+    (33, 20011, 64, 0.0, 1.0, torch.int32),
     (5, 300, 72, 0.4, 1.0, torch.int64),
     (128, 257, 128, 0.0, 0.8, torch.int32),
     (129, 511, 136, 0.5, 1.0, torch.int32),
