@@ -630,7 +630,8 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
                       misaligned(x.v, sa) || misaligned(x.master, 32));
         master = master || x.master;
         a.first_cta[i - begin] = static_cast<int>(ctas);
-        ctas += (x.n + per_cta - 1) / per_cta;       // under 2^31: n < 2^34 and 8192 elements a CTA for long lists
+        ctas += (x.n + per_cta - 1) / per_cta;
+        if (ctas > 0x7fffffffLL) return DG_EINVAL;   // over 2^42 elements
     }
     a.first_cta[end - begin] = static_cast<int>(ctas);
     if (ctas == 0) return DG_OK;
@@ -701,12 +702,14 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     }
     // a master copy for all tensors of a call or for none, and only beside bf16 parameters that it rounds to
     if (with_master != 0 && (with_master != live || p->param_type != DG_BF16 || p->stochastic)) return DG_EINVAL;
-    // Few elements: one block a warp, to spread them over the SMs.  Many: 8 blocks a warp, which share the
-    // search of the list and the constants (120 million bf16 parameters, 8-bit states: 0.311 ms with 8, 0.320
-    // with 4).
+    // 8-bit states of many elements: 8 blocks a warp, which share the search of the list, the constants and the
+    // exponents' accesses (262144 x 2816 bf16 parameters: 1.86 ms with 8, 1.92 with 4, 2.25 with 1).  fp32 states
+    // (bound by the bytes; 65536 x 2816 with master: 0.751 ms with 1, 0.799 with 8) and few elements (to spread
+    // them over the SMs): one.
     const int sms = device_sm_count();
     if (sms <= 0) return DG_ECUDA;
-    const int bpw = total > static_cast<long long>(sms) * 8 * kWarps * kBlock * kMaxBlocksPerWarp ? kMaxBlocksPerWarp : 1;
+    const bool many = total > static_cast<long long>(sms) * 8 * kWarps * kBlock * kMaxBlocksPerWarp;
+    const int bpw = p->state_bits == 8 && many ? kMaxBlocksPerWarp : 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launches = 0;
     for (int begin = 0; begin < n_tensors;) {

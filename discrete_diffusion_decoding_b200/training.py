@@ -177,7 +177,9 @@ def head_cross_entropy(h, W, targets, temperature=1.0, ignore_index=-100):
     """Cross entropy of softmax(h W^T / temperature) at `targets`, per position, differentiable in h and W.
 
     h [..., d] bf16, W [V, d] bf16, targets [...] int32 or int64.  Returns float32 [...]: 0 where the target
-    is ignore_index.  No logits are stored; weight or average the result as the objective asks.
+    is ignore_index.  No logits are stored; weight or average the result as the objective asks.  dh and dW are
+    bf16.  Both directions can be captured into a CUDA graph as any autograd function can: after a warm-up on
+    the capturing stream, with no eager graph of the same leaves alive.
     """
     fn = "head_cross_entropy"
     if h.dim() < 1 or W.dim() != 2 or tuple(h.shape[:-1]) != tuple(targets.shape) or h.shape[-1] != W.shape[1]:
@@ -241,7 +243,7 @@ class AdamWTensors:
             _refuse(fn, "the lists differ in length")
         state = torch.uint8 if bits8 else torch.float32
         self.param_type, self.state_bits = _TYPES[ptype], 8 if bits8 else 32
-        self.params = params
+        self.params, self.master = params, lists.get("master")
         self.held = [params] + list(lists.values())
         self.table = (DgAdamWTensor * k)()
         spans = []
@@ -340,15 +342,24 @@ class AdamW:
         if len(grads) != len(self.params):
             _refuse("AdamW.step", "grads has another length than params")
         for at, tensors in self.groups:
+            for i, row in zip(at, tensors.table):
+                if self.params[i].data_ptr() != (row.param or 0):
+                    _refuse("AdamW.step", f"parameter {i} lies elsewhere than when the optimizer was made")
             tensors.set_grads([grads[i] for i in at])
-        self.steps += 1
         for k, (_, tensors) in enumerate(self.groups):
             plain_bf16 = tensors.param_type == _abi.DG_BF16 and not tensors.table[0].master
             # a key of its own for each list, whose tensors count from 0
-            p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, step=self.steps,
+            p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, step=self.steps + 1,
                              grad_scale=grad_scale, seed=(self.seed + (k << 63)) & (1 << 64) - 1,
                              stochastic=int(plain_bf16))
             dg_adamw_step(p, tensors, stream)
+        self.steps += 1
+
+    def refresh_master(self):
+        """Take the 32-bit master copies from the parameters again (after they were loaded or changed)."""
+        for at, tensors in self.groups:
+            for i, m in zip(at, tensors.master or ()):
+                m.copy_(self.params[i].detach())
 
     def zero_grad(self):
         for p in self.params:
@@ -382,8 +393,10 @@ class HeadTrainer:
 
     def __init__(self, W, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,
                  grad_dtype=torch.bfloat16, temperature=1.0, ignore_index=-100, seed=0):
-        if W.dim() != 2:
-            _refuse("HeadTrainer", f"W has shape {tuple(W.shape)}, expected [V, d]")
+        if W.dim() != 2 or W.dtype != torch.bfloat16 or not W.is_contiguous():
+            _refuse("HeadTrainer", f"W is {W.dtype} {tuple(W.shape)}, expected a dense torch.bfloat16 [V, d]")
+        if grad_dtype not in _TYPES:
+            _refuse("HeadTrainer", f"grad_dtype is {grad_dtype}, expected bfloat16 or float32")
         self.W = W.detach()
         self.optimizer = AdamW([self.W], lr, betas, eps, weight_decay, state_bits, master, seed)
         self.dW = torch.empty(W.shape, dtype=grad_dtype, device=W.device)

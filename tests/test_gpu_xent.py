@@ -372,10 +372,8 @@ def test_refusals_on_the_device(dg):
             dg.XentWorkspace(q)
 
 
-def test_a_wait_that_ran_out_gives_nan(dg):
-    """The kernels' error word, set between the products and the last launch, is not reachable from outside;
-    what can be set is the word's effect: the merge of a workspace whose word is raised is covered by the
-    kernels that read it.  Here: a call clears the word that an earlier call left."""
+def test_a_call_clears_the_error_word_of_an_earlier_one(dg):
+    """A raised error word (a wait that ran out) in a workspace does not reach the next call with it."""
     h, W, y, dl = inputs(20, 600, 64)
     p = dg.xent_params(20, 600, 64)
     ws = dg.XentWorkspace(p)
