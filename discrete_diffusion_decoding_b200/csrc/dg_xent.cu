@@ -229,6 +229,7 @@ struct GemmArgs {
     CUtensorMap h_k, w_k;            // packed h (n rows: those behind are zeros that nothing reads) and W, K-major: logits
     CUtensorMap g_k, w_mn;           // G K-major, W MN-major: dh
     CUtensorMap g_mn, h_mn;          // G and packed h, MN-major: dW
+    CUtensorMap g_out, dw_out;       // G and a bf16 dW as outputs, boxes of 64 columns x 32 rows
     Packed pk;
     uint32_t* ticket;                // this launch's counter
     int vocab, d, d_tiles;
@@ -243,8 +244,6 @@ struct GemmArgs {
     int wide;                        // a kind of at least so many tiles goes in twos
     int tail;                        // but about so many of the last kind's
     int first_piece, want_dh, want_dw;
-    __nv_bfloat16* g;                // [2][g_rows][piece]
-    int piece;
     float* slab;                     // [splits][slab_rows][d] fp32 sums of dh
     void* dw;
     int dw_fp32, dw_accumulate;
@@ -358,9 +357,9 @@ __device__ __forceinline__ bool group_any(int group, bool mine) {
 
 __device__ __forceinline__ void group_bar(int group) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + group) : "memory"); }
 
-// A warp's 32 rows x 128 bytes through shared memory: written by rows (thread = row), read as 4 rows of 8 lanes x
-// 16 bytes, so that an access to global memory covers whole lines (16 bytes of 32 rows a time, dh's tiles took 8
-// us and dW's 2.9).  Chunk c of row r lies at c ^ (r % 8): no bank conflicts either way.
+// A warp's 32 rows x 128 bytes go through shared memory, written by rows (thread = row): bf16 ones leave by TMA,
+// fp32 ones are read back as 4 rows of 8 lanes x 16 bytes, so that an access to global memory covers whole lines
+// (with 16 bytes of 32 rows a time, dh's tiles took 8 us and dW's 2.9).  Chunk c of row r lies at c ^ (r % 8): no bank conflicts either way.
 __device__ __forceinline__ void row_chunk(uint32_t own, int row, int chunk, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + row * 128 + ((chunk ^ (row & 7)) << 4)), "r"(a),
                  "r"(b), "r"(c), "r"(d)
@@ -376,34 +375,45 @@ __device__ __forceinline__ uint4 line_chunk(uint32_t own, int row, int chunk) {
     return v;
 }
 
-// 64 bf16 columns of the warp's rows: out is the first row's first column, rows_left and cols_left what lies inside.
-// `value` takes the place of this thread's column `at` where that is one of the 64.
-__device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t* r, __nv_bfloat16* out,
-                                          long long stride, int rows_left, int cols_left, int at = -1,
-                                          float value = 0.f) {
+// Shared memory -> a box of an output map; completion by bulk groups.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(src), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 64 bf16 columns of the warp's rows as one box of `map` at column x, row y, which the copy clips to the matrix
+// (inside: it starts in it).  `value` takes the place of this thread's column `at` where that is one of the 64.
+__device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t* r, const CUtensorMap* map, int x, int y,
+                                          bool inside, int at = -1, float value = 0.f) {
+    uint32_t u[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) u[k] = bf16_pair(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+    if (lane == 0) bulk_wait_read();          // the copy before this one has read the rows
     __syncwarp();
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-        row_chunk(own, lane, c, bf16_pair(__uint_as_float(r[8 * c]), __uint_as_float(r[8 * c + 1])),
-                  bf16_pair(__uint_as_float(r[8 * c + 2]), __uint_as_float(r[8 * c + 3])),
-                  bf16_pair(__uint_as_float(r[8 * c + 4]), __uint_as_float(r[8 * c + 5])),
-                  bf16_pair(__uint_as_float(r[8 * c + 6]), __uint_as_float(r[8 * c + 7])));
+    for (int c = 0; c < 8; ++c) row_chunk(own, lane, c, u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
     if (at >= 0 && at < 64)
         asm volatile("st.shared.b16 [%0], %1;" ::"r"(own + lane * 128 + (((at >> 3) ^ (lane & 7)) << 4) + (at & 7) * 2),
                      "h"(static_cast<unsigned short>(bf16_pair(value, 0.f)))
                      : "memory");
+    fence_async_shared();
     __syncwarp();
-    const int c = lane & 7;
-    out += (lane >> 3) * stride + c * 8;
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        if (4 * q + (lane >> 3) < rows_left && c * 8 < cols_left)
-            *reinterpret_cast<uint4*>(out + 4 * q * stride) = line_chunk(own, 4 * q + (lane >> 3), c);
+    if (lane == 0 && inside) {
+        tma_store_2d(map, own, x, y);
+        bulk_commit();
+    }
 }
 
 // 32 fp32 columns (r[at], ...) of the warp's rows, each 4 given to put(row, first column, values).
 template <class Put>
 __device__ __forceinline__ void rows_fp32(uint32_t own, int lane, const uint32_t* r, int rows_left, int cols_left, Put put) {
+    if (lane == 0) bulk_wait_read();
     __syncwarp();
 #pragma unroll
     for (int c = 0; c < 8; ++c) row_chunk(own, lane, c, r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
@@ -458,9 +468,9 @@ __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint3
             if (!live || n0 + k >= limit) r[k] = 0;
     }
     const float tcoef = off >= 0 && off < kHalf ? a.pk.tcoef[i] : 0.f;
-    __nv_bfloat16* out = a.g + (static_cast<long long>(a.g_write) * a.g_rows + i - lane) * a.piece + n0;
 #pragma unroll
-    for (int c = 0; c < kHalf; c += 64) rows_bf16(own, lane, &r[c], out + c, a.piece, 32, 64, off - c, tcoef);
+    for (int c = 0; c < kHalf; c += 64)
+        rows_bf16(own, lane, &r[c], &a.g_out, n0 + c, a.g_write * a.g_rows + i - lane, true, off - c, tcoef);
 }
 
 // This row's half of a dh tile: added to (first piece: stored in) the split's fp32 slab.  Each address is touched
@@ -493,7 +503,7 @@ __device__ __forceinline__ void dw_epilogue(const GemmArgs& a, int n0, uint32_t 
     if (!a.dw_fp32 && !a.dw_accumulate) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 64)
-            rows_bf16(own, lane, &r[c], static_cast<__nv_bfloat16*>(a.dw) + first + c, a.d, rows_left, a.d - (n0 + c));
+            rows_bf16(own, lane, &r[c], &a.dw_out, n0 + c, v - lane, rows_left > 0 && n0 + c < a.d);
         return;
     }
 #pragma unroll
@@ -824,6 +834,7 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
             }
             if (it.tiles == 1) next ^= 1;
         }
+        if (lane == 0) bulk_wait();          // the copies out have been made
     }
     __syncwarp();
     tc_fence_before();
@@ -1423,8 +1434,6 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     ga.kb_per_split = q.kb_per_split;
     ga.want_dh = dh_dev != nullptr;
     ga.want_dw = dW_dev != nullptr;
-    ga.g = static_cast<__nv_bfloat16*>(g);
-    ga.piece = q.piece;
     ga.slab = slab;
     ga.dw = dW_dev;
     ga.dw_fp32 = p->dw_type == DG_FP32;
@@ -1432,7 +1441,9 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     const uint64_t rows = q.rows_alloc, d = p->hidden;
     if (!encode_2d(&ga.h_k, ga.pk.h, p->n, d, kHalf) || !encode_2d(&ga.h_mn, ga.pk.h, rows, d, kK) ||
         !encode_2d(&ga.w_k, W_dev, p->vocab, d, kHalf) || !encode_2d(&ga.w_mn, W_dev, p->vocab, d, kK) ||
-        !encode_2d(&ga.g_k, g, 2 * rows, q.piece, kHalf) || !encode_2d(&ga.g_mn, g, 2 * rows, q.piece, kK))
+        !encode_2d(&ga.g_k, g, 2 * rows, q.piece, kHalf) || !encode_2d(&ga.g_mn, g, 2 * rows, q.piece, kK) ||
+        !encode_2d(&ga.g_out, g, 2 * rows, q.piece, 32) ||
+        (dW_dev && !ga.dw_fp32 && !encode_2d(&ga.dw_out, dW_dev, p->vocab, d, 32)))
         return DG_ECUDA;
     // the kinds of tiles, longest contraction first
     const int length[3] = {(p->hidden + kK - 1) / kK, q.kb_per_split, (p->n + kK - 1) / kK};
