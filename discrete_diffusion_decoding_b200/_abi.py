@@ -33,7 +33,7 @@ class DgXentParams(ctypes.Structure):
     _fields_ = [("n", ctypes.c_int), ("vocab", ctypes.c_int), ("hidden", ctypes.c_int),
                 ("temperature", ctypes.c_float), ("ignore_index", ctypes.c_longlong),
                 ("h_stride", ctypes.c_longlong), ("target_type", ctypes.c_int), ("dw_type", ctypes.c_int),
-                ("dw_accumulate", ctypes.c_int)]
+                ("dw_accumulate", ctypes.c_int), ("scratch_bytes", ctypes.c_longlong)]
 
 
 class DgAdamWParams(ctypes.Structure):

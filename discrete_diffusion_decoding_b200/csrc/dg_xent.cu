@@ -1116,6 +1116,7 @@ struct XentPlan {
 };
 
 constexpr int kMaxRows = 1 << 22;
+constexpr long long kScratchBytes = 400LL << 20;     // of G in the backward, where the caller names no other
 
 dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     if (!p || p->n < 0 || p->vocab < 1 || p->hidden < 1) return DG_EINVAL;
@@ -1124,6 +1125,7 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     if (p->dw_type != DG_BF16 && p->dw_type != DG_FP32) return DG_EINVAL;
     if (p->dw_accumulate != 0 && p->dw_accumulate != 1) return DG_EINVAL;
     if (p->h_stride != 0 && p->h_stride < p->hidden) return DG_EINVAL;
+    if (p->scratch_bytes < 0) return DG_EINVAL;
     // a TMA row starts on 16 bytes; the counts below stay in 32 bits
     if (p->hidden % 8 != 0 || p->hidden > 65536 || p->n > kMaxRows || p->vocab > (1 << 28)) return DG_EUNSUPPORTED;
     const int sms = host::device_sm_count();
@@ -1156,14 +1158,15 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
         const size_t of_few = p->n <= kFewRows ? sizeof(float2) * 8 * q.pairs * kFewRows : 0;
         q.part = take(16 * n * q.v_tiles > of_few ? 16 * n * q.v_tiles : of_few);
     } else {
-        // A piece's rows of W in at most 48 MB and its two buffers of G in at most 96 MB, so that most of what
-        // a launch reads again is in L2; no more than the vocabulary, no less than 1024 columns.
-        long long piece = (400LL << 20) / (2 * static_cast<long long>(p->hidden));
-        const long long of_g = (400LL << 20) / (4 * static_cast<long long>(q.rows_alloc > 0 ? q.rows_alloc : 1));
-        if (piece > of_g) piece = of_g;
-        piece = piece / kTile * kTile;
-        if (piece < 1024) piece = 1024;
-        if (piece > static_cast<long long>(q.v_tiles) * kTile) piece = static_cast<long long>(q.v_tiles) * kTile;
+        // The whole vocabulary in one piece where G fits the scratch, else pieces whose two buffers do (fewer and
+        // longer launches: a training step of 256 positions, V = 262144, d = 2816 took 2.3 ms in pieces of 8704
+        // columns, 1.9 ms in pieces of 70000; of 4096 positions 22.5 ms in pieces of 5888, 21.5 ms of 25600).
+        const long long scratch = p->scratch_bytes > 0 ? p->scratch_bytes : kScratchBytes;
+        const long long column = 2 * static_cast<long long>(q.rows_alloc > 0 ? q.rows_alloc : 1);
+        const long long all = static_cast<long long>(q.v_tiles) * kTile;
+        long long piece = scratch / (2 * column) / kTile * kTile;
+        if (piece < kTile) piece = kTile;
+        if (all <= piece || all <= scratch / column) piece = all;
         q.piece = static_cast<int>(piece);
         q.pieces = (p->vocab + q.piece - 1) / q.piece;
         // dh: about one item (two tiles) for every pair, split along the vocabulary into no less than 8 stages
@@ -1175,7 +1178,7 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
         q.kb_per_split = (kbs + splits - 1) / splits;
         q.splits = (kbs + q.kb_per_split - 1) / q.kb_per_split;
         q.tickets = take(4 * static_cast<size_t>(q.pieces + 1));
-        q.g = take(2 * 2 * n * q.piece);
+        q.g = take((q.pieces > 1 ? 4 : 2) * n * q.piece);
         q.slab = take(4 * n * p->hidden * q.splits);
     }
     q.total = o;
@@ -1438,11 +1441,11 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     ga.dw = dW_dev;
     ga.dw_fp32 = p->dw_type == DG_FP32;
     ga.dw_accumulate = p->dw_accumulate;
-    const uint64_t rows = q.rows_alloc, d = p->hidden;
+    const uint64_t rows = q.rows_alloc, d = p->hidden, g_rows = q.pieces > 1 ? 2 * rows : rows;
     if (!encode_2d(&ga.h_k, ga.pk.h, p->n, d, kHalf) || !encode_2d(&ga.h_mn, ga.pk.h, rows, d, kK) ||
         !encode_2d(&ga.w_k, W_dev, p->vocab, d, kHalf) || !encode_2d(&ga.w_mn, W_dev, p->vocab, d, kK) ||
-        !encode_2d(&ga.g_k, g, 2 * rows, q.piece, kHalf) || !encode_2d(&ga.g_mn, g, 2 * rows, q.piece, kK) ||
-        !encode_2d(&ga.g_out, g, 2 * rows, q.piece, 32) ||
+        !encode_2d(&ga.g_k, g, g_rows, q.piece, kHalf) || !encode_2d(&ga.g_mn, g, g_rows, q.piece, kK) ||
+        !encode_2d(&ga.g_out, g, g_rows, q.piece, 32) ||
         (dW_dev && !ga.dw_fp32 && !encode_2d(&ga.dw_out, dW_dev, p->vocab, d, 32)))
         return DG_ECUDA;
     // the kinds of tiles, longest contraction first

@@ -377,7 +377,7 @@ enum { DG_INT32 = 0, DG_INT64 = 1 };
 
 /*
  * Cross entropy of a head W [vocab, hidden] at n positions.  Limits: n >= 0, vocab >= 1,
- * temperature > 0 and finite (DG_EINVAL otherwise); hidden a multiple of 8 up to 65536,
+ * temperature > 0 and finite, scratch_bytes >= 0 (DG_EINVAL otherwise); hidden a multiple of 8 up to 65536,
  * n up to 2^22, vocab up to 2^28 (DG_EUNSUPPORTED otherwise).
  */
 typedef struct {
@@ -390,6 +390,9 @@ typedef struct {
     int target_type;        /* DG_INT32 or DG_INT64 */
     int dw_type;            /* type of dW: DG_BF16 or DG_FP32 */
     int dw_accumulate;      /* 1: dW is added to what dW_dev holds; 0: it overwrites it */
+    long long scratch_bytes;/* the part of the backward's workspace that holds G, a piece of the
+                             * vocabulary at a time (never less than two pieces of 256 columns
+                             * take); 0 = 400 MiB.  Another value may change dh's last bits */
 } dg_xent_params;
 
 /* temperature 1, ignore_index -100, dense h, int32 targets, bf16 dW, overwrite. */
@@ -427,6 +430,7 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
  *   dW_dev:    [vocab, hidden] bf16 or fp32 (dw_type), 16-byte aligned (NULL: not wanted)
  * At least one of dh_dev and dW_dev (DG_EINVAL); neither may overlap W, nor dh h (DG_EINVAL).
  * n = 0 zeroes dW unless dw_accumulate.  The results of equal calls are equal to the bit.
+ * Launches: three and one for every piece (see scratch_bytes).
  * A wait that runs out makes both gradients NaN.
  */
 dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const void* W_dev, const void* targets_dev,

@@ -90,10 +90,19 @@ def test_loss_and_gradients(dg, n, V, d, ignored, T, index):
     check(h, W, y, dl, T, run(dg, h, W, y, dl, T))
 
 
-@pytest.mark.parametrize("n,V,d", [(40, 40000, 64), (1030, 18001, 96)])
-def test_several_pieces_of_the_vocabulary(dg, n, V, d):
+@pytest.mark.parametrize("n,V,d,scratch,pieces", [
+    (40, 40000, 64, 0, 1),
+    (40, 4000, 64, 1, 16),                      # a tile of columns at a time
+    (300, 5000, 136, 2 * 2 * 512 * 1024, 5),
+    (1030, 18001, 96, 2 * 2 * 1280 * 7000, 3),
+    (257, 1281, 72, 2 * 512 * 1280, 3),         # one column more than fits at once
+    (257, 1280, 72, 2 * 512 * 1280, 1),
+])
+def test_pieces_of_the_vocabulary(dg, n, V, d, scratch, pieces):
     h, W, y, dl = inputs(n, V, d, seed=3, ignored=0.2)
-    check(h, W, y, dl, 1.0, run(dg, h, W, y, dl))
+    got = run(dg, h, W, y, dl, scratch_bytes=scratch)
+    assert dg.last_launch_count() == 3 + pieces
+    check(h, W, y, dl, 1.0, got)
 
 
 def test_confident_positions_keep_their_digits(dg):
@@ -365,7 +374,7 @@ def test_refusals_on_the_device(dg):
     for grads in ((None, None), (hd, dW), (dh, Wd), (Wd[:20], dW), (dh.float(), dW), (dh, dW.half())):
         with pytest.raises(dg.DgError):
             dg.dg_xent_backward(p, hd, Wd, yd, loss, lse, dld, *grads, ws)
-    for k, v in (("temperature", 0.0), ("temperature", float("nan")), ("dw_accumulate", 2), ("hidden", 60)):
+    for k, v in (("temperature", 0.0), ("temperature", float("nan")), ("dw_accumulate", 2), ("hidden", 60), ("scratch_bytes", -1)):
         q = dg.xent_params(20, 600, 64)
         setattr(q, k, v)
         with pytest.raises(dg.DgError):
