@@ -387,10 +387,10 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-// 64 bf16 columns of the warp's rows as one box of `map` at column x, row y, which the copy clips to the matrix
-// (inside: it starts in it).  `value` takes the place of this thread's column `at` where that is one of the 64.
+// 64 bf16 columns of the warp's rows as one box of `map` that starts inside at column x, row y (the copy clips it
+// to the matrix).  `value` takes the place of this thread's column `at` where that is one of the 64.
 __device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t* r, const CUtensorMap* map, int x, int y,
-                                          bool inside, int at = -1, float value = 0.f) {
+                                          int at = -1, float value = 0.f) {
     uint32_t u[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) u[k] = bf16_pair(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
@@ -404,7 +404,7 @@ __device__ __forceinline__ void rows_bf16(uint32_t own, int lane, const uint32_t
                      : "memory");
     fence_async_shared();
     __syncwarp();
-    if (lane == 0 && inside) {
+    if (lane == 0) {
         tma_store_2d(map, own, x, y);
         bulk_commit();
     }
@@ -455,22 +455,30 @@ __device__ __forceinline__ void loss_epilogue(const GemmArgs& a, int n0, uint32_
 // This row's half tile of logits -> its entries of G in bf16; rows and columns outside are 0.
 __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint32_t (&r)[kHalf], int i, int rows,
                                                 uint32_t own, int lane) {
+    // rows that no later product reads (dW's sums end with the stage of the last position) are not written
+    if (i - lane >= (rows + kK - 1) / kK * kK) return;
     const bool live = i < rows;
     const int limit = a.vocab - a.v0_logits;
     const float coef = live ? a.pk.coef[i] : 0.f, lse2 = live ? a.pk.lse2[i] : 0.f;
     const int off = live ? a.pk.target[i] - a.v0_logits - n0 : -1;
-#pragma unroll
-    for (int k = 0; k < kHalf; ++k)
-        r[k] = __float_as_uint(exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -lse2)) * coef);
-    if (!live || n0 + kHalf > limit) {
+    if (i - lane < rows) {
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
-            if (!live || n0 + k >= limit) r[k] = 0;
+            r[k] = __float_as_uint(exp2_sfu(fmaf(__uint_as_float(r[k]), a.scale_log2, -lse2)) * coef);
+    }
+    if (!live) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k) r[k] = 0;
+    }
+    if (n0 + kHalf > limit) {
+#pragma unroll
+        for (int k = 0; k < kHalf; ++k)
+            if (n0 + k >= limit) r[k] = 0;
     }
     const float tcoef = off >= 0 && off < kHalf ? a.pk.tcoef[i] : 0.f;
 #pragma unroll
     for (int c = 0; c < kHalf; c += 64)
-        rows_bf16(own, lane, &r[c], &a.g_out, n0 + c, a.g_write * a.g_rows + i - lane, true, off - c, tcoef);
+        rows_bf16(own, lane, &r[c], &a.g_out, n0 + c, a.g_write * a.g_rows + i - lane, off - c, tcoef);
 }
 
 // This row's half of a dh tile: added to (first piece: stored in) the split's fp32 slab.  Each address is touched
@@ -478,9 +486,10 @@ __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint3
 __device__ __forceinline__ void dh_epilogue(const GemmArgs& a, int n0, int split, const uint32_t (&r)[kHalf], int i,
                                             int rows, uint32_t own, int lane) {
     float* out = a.slab + (static_cast<long long>(split) * a.slab_rows + i - lane) * a.d + n0;
+    if (i - lane >= rows) return;
 #pragma unroll
     for (int c = 0; c < kHalf; c += 32)
-        rows_fp32(own, lane, &r[c], rows - (i - lane), a.d - (n0 + c), [&](int row, int col, const float4& x) {
+        if (n0 + c < a.d) rows_fp32(own, lane, &r[c], rows - (i - lane), a.d - (n0 + c), [&](int row, int col, const float4& x) {
             float* to = out + static_cast<long long>(row) * a.d + c + col;
             if (a.first_piece)
                 *reinterpret_cast<float4*>(to) = x;
@@ -503,12 +512,12 @@ __device__ __forceinline__ void dw_epilogue(const GemmArgs& a, int n0, uint32_t 
     if (!a.dw_fp32 && !a.dw_accumulate) {
 #pragma unroll
         for (int c = 0; c < kHalf; c += 64)
-            rows_bf16(own, lane, &r[c], &a.dw_out, n0 + c, v - lane, rows_left > 0 && n0 + c < a.d);
+            if (rows_left > 0 && n0 + c < a.d) rows_bf16(own, lane, &r[c], &a.dw_out, n0 + c, v - lane);
         return;
     }
 #pragma unroll
     for (int c = 0; c < kHalf; c += 32)
-        rows_fp32(own, lane, &r[c], rows_left, a.d - (n0 + c), [&](int row, int col, float4 x) {
+        if (n0 + c < a.d) rows_fp32(own, lane, &r[c], rows_left, a.d - (n0 + c), [&](int row, int col, float4 x) {
             const long long at = first + static_cast<long long>(row) * a.d + c + col;
             if (a.dw_fp32) {
                 float4* to = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + at);
@@ -1093,7 +1102,7 @@ __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const fl
         const int i = static_cast<int>(k / vecs), c = static_cast<int>(k % vecs) * 4;
         const float* src = slab + static_cast<long long>(i) * d + c;
         float x[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 16
         for (int s = 0; s < splits; ++s) {
             const float4 u = __ldg(reinterpret_cast<const float4*>(src + s * slab_stride));
             x[0] += u.x;
