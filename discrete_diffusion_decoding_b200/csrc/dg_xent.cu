@@ -58,7 +58,7 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiBytes = 4096;            // an epilogue warp's rows on their way out: 32 x 128 bytes
 constexpr int kSmemBytes = kBoxes * kOperand + 8 * kEpiBytes + 1024;
 constexpr int kSched = 2;                  // items in hand: the one in work and the next
-constexpr int kPackRows = 8;               // rows per CTA of the gather
+constexpr int kPackRows = 8;               // rows a CTA of the gather looks at together
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -92,7 +92,7 @@ struct Packed {
     float* coef;         // backward: dloss / T
     float* tcoef;        // backward: the target's entry of G
     __nv_bfloat16* h;    // [rounded up to 256 rows, d]; zeros up to a multiple of 64 rows
-    uint32_t* tickets;   // one counter of tiles for each launch of products
+    uint32_t* tickets;   // one counter of items for each launch of products
     int n_tickets;
 };
 
@@ -105,6 +105,7 @@ struct PackArgs {
     int targets64;
     long long ignore;
     int n, d, vocab;
+    int rows_per_cta;        // a multiple of 8
     float inv_t, scale_log2;
     const float* loss_in;    // backward inputs (null in the forward)
     const float* lse_in;
@@ -133,12 +134,13 @@ __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc)
     return acc;
 }
 
-// CTA b looks at rows [8 b, 8 b + 8), a warp at one.  Each CTA counts the kept positions before its rows (and
-// all of them) itself: N / 256 coalesced reads a thread from L2, cheaper than a scan launch before this one.
+// A CTA looks at rows_per_cta rows, 8 at a time, a warp at one.  Each CTA counts the kept positions before its
+// rows (and all of them) itself: N / 256 coalesced reads a thread from L2, cheaper than a scan launch before this
+// one (8 rows a CTA up to 16384 positions; more rows for more, so that these reads stay linear in N).
 __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
     __shared__ int warp_before[8], warp_all[8];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r0 = blockIdx.x * kPackRows;
+    const int r0 = blockIdx.x * a.rows_per_cta;
     griddep_launch();
     griddep_wait();
     int before = 0, all = 0;
@@ -168,57 +170,59 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
         }
         for (int i = tid; i < a.out.n_tickets; i += 256) a.out.tickets[i] = 0;
     }
-    // lanes 0..7 look at the CTA's rows; every warp does, for its own row's place
-    long long y = 0;
-    const bool k = lane < kPackRows && r0 + lane < a.n && counts(a, r0 + lane, y);
-    const uint32_t kept = __ballot_sync(0xffffffffu, k);
-    const int i = r0 + warp, at = before + __popc(kept & ((1u << warp) - 1u));
-    const bool mine = kept >> warp & 1u;
-    y = __shfl_sync(0xffffffffu, y, warp);
-    // the rows behind the last one kept, up to a whole stage of the products that sum over positions
-    if (i >= all && i < (all + kK - 1) / kK * kK) zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
-    if (i >= a.n) return;
-    if (!mine) {
-        if (lane == 0 && a.loss_out) {
-            a.loss_out[i] = 0.f;
-            if (a.lse_out) a.lse_out[i] = 0.f;
-        }
-        if (a.dh) zero_row(a.dh + static_cast<long long>(i) * a.d, a.d, lane);
-        return;
-    }
-    const bool inside = y >= 0 && y < a.vocab;
-    const __nv_bfloat16* src = a.h + static_cast<long long>(i) * a.h_stride;
-    __nv_bfloat16* dst = a.out.h + static_cast<long long>(at) * a.d;
     const bool vec = (reinterpret_cast<uintptr_t>(a.h) & 15) == 0 && (a.h_stride & 7) == 0;
-    if (vec) {
+    for (int r = r0; r < r0 + a.rows_per_cta; r += kPackRows) {
+        // lanes 0..7 look at these rows; every warp does, for its own row's place
+        long long y = 0;
+        const bool k = lane < kPackRows && r + lane < a.n && counts(a, r + lane, y);
+        const uint32_t kept = __ballot_sync(0xffffffffu, k);
+        const int i = r + warp, at = before + __popc(kept & ((1u << warp) - 1u));
+        before += __popc(kept);
+        y = __shfl_sync(0xffffffffu, y, warp);
+        // the rows behind the last one kept, up to a whole stage of the products that sum over positions
+        if (i >= all && i < (all + kK - 1) / kK * kK) zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
+        if (i >= a.n) continue;
+        if (!(kept >> warp & 1u)) {
+            if (lane == 0 && a.loss_out) {
+                a.loss_out[i] = 0.f;
+                if (a.lse_out) a.lse_out[i] = 0.f;
+            }
+            if (a.dh) zero_row(a.dh + static_cast<long long>(i) * a.d, a.d, lane);
+            continue;
+        }
+        const bool inside = y >= 0 && y < a.vocab;
+        const __nv_bfloat16* src = a.h + static_cast<long long>(i) * a.h_stride;
+        __nv_bfloat16* dst = a.out.h + static_cast<long long>(at) * a.d;
+        if (vec) {
 #pragma unroll 4
-        for (int c = lane * 8; c < a.d; c += 256)
-            *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(src + c));
-    } else {
-#pragma unroll 4
-        for (int c = lane; c < a.d; c += 32) dst[c] = __ldg(src + c);
-    }
-    float zt = 0.f;
-    if (!a.dloss && inside) {
-        // read back what this warp has just written: the same values, whatever h's alignment
-        __syncwarp();
-        const __nv_bfloat16* w = a.W + y * a.d;
-#pragma unroll 4
-        for (int c = lane * 8; c < a.d; c += 256)
-            zt = dot8(*reinterpret_cast<const uint4*>(dst + c), __ldg(reinterpret_cast<const uint4*>(w + c)), zt);
-#pragma unroll
-        for (int off = 16; off; off >>= 1) zt += __shfl_xor_sync(0xffffffffu, zt, off);
-    }
-    if (lane == 0) {
-        a.out.row[at] = i;
-        a.out.target[at] = inside ? static_cast<int32_t>(y) : -1;
-        if (a.dloss) {
-            const float c = inside ? a.dloss[i] * a.inv_t : NAN;
-            a.out.coef[at] = c;
-            a.out.tcoef[at] = c * expm1f(-a.loss_in[i]);
-            a.out.lse2[at] = a.lse_in[i] * kLog2e;
+            for (int c = lane * 8; c < a.d; c += 256)
+                *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(src + c));
         } else {
-            a.out.zt2[at] = zt * a.scale_log2;
+#pragma unroll 4
+            for (int c = lane; c < a.d; c += 32) dst[c] = __ldg(src + c);
+        }
+        float zt = 0.f;
+        if (!a.dloss && inside) {
+            // read back what this warp has just written: the same values, whatever h's alignment
+            __syncwarp();
+            const __nv_bfloat16* w = a.W + y * a.d;
+#pragma unroll 4
+            for (int c = lane * 8; c < a.d; c += 256)
+                zt = dot8(*reinterpret_cast<const uint4*>(dst + c), __ldg(reinterpret_cast<const uint4*>(w + c)), zt);
+#pragma unroll
+            for (int off = 16; off; off >>= 1) zt += __shfl_xor_sync(0xffffffffu, zt, off);
+        }
+        if (lane == 0) {
+            a.out.row[at] = i;
+            a.out.target[at] = inside ? static_cast<int32_t>(y) : -1;
+            if (a.dloss) {
+                const float c = inside ? a.dloss[i] * a.inv_t : NAN;
+                a.out.coef[at] = c;
+                a.out.tcoef[at] = c * expm1f(-a.loss_in[i]);
+                a.out.lse2[at] = a.lse_in[i] * kLog2e;
+            } else {
+                a.out.zt2[at] = zt * a.scale_log2;
+            }
         }
     }
 }
@@ -1283,7 +1287,8 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 
 dg_status launch_pack(const PackArgs& in, cudaStream_t s) {
     const int rows = (in.n + kK - 1) / kK * kK;
-    return launch_next(dg_xent_pack_kernel, rows / kPackRows, 256, 1, 0, s, in) == cudaSuccess ? DG_OK : DG_ECUDA;
+    const int grid = (rows + in.rows_per_cta - 1) / in.rows_per_cta;
+    return launch_next(dg_xent_pack_kernel, grid, 256, 1, 0, s, in) == cudaSuccess ? DG_OK : DG_ECUDA;
 }
 
 PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const void* h, const void* W,
@@ -1300,6 +1305,7 @@ PackArgs pack_args(const dg_xent_params* p, const XentPlan& q, void* ws, const v
     a.n = p->n;
     a.d = p->hidden;
     a.vocab = p->vocab;
+    a.rows_per_cta = kPackRows * ((p->n + 2048 * kPackRows - 1) / (2048 * kPackRows));
     a.inv_t = static_cast<float>(1.0 / static_cast<double>(p->temperature));
     a.scale_log2 = static_cast<float>(1.4426950408889634 / static_cast<double>(p->temperature));
     return a;

@@ -302,7 +302,8 @@ class AdamW:
 
     bf16 parameters keep a 32-bit master copy (`master`) or are rounded at random without one; `weight_decay`
     is one value or one for each parameter.  Steps take the parameters' .grad, or the list given to step();
-    a parameter without a gradient is left as it is.
+    a parameter without a gradient is left as it is.  (A captured step repeats the count and the rate of its
+    capture: graphs take dg_adamw_step with step_dev and lr_dev instead.)
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,

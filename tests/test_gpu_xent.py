@@ -105,6 +105,34 @@ def test_pieces_of_the_vocabulary(dg, n, V, d, scratch, pieces):
     check(h, W, y, dl, 1.0, got)
 
 
+@pytest.mark.parametrize("n,V,d,ignored,scratch", [
+    (7, 80000, 72, 0.0, 0), (1, 76000, 8, 0.0, 0), (65, 20100, 1000, 0.2, 0), (256, 30001, 520, 0.0, 0),
+    (257, 30001, 520, 0.0, 0), (128, 40000, 264, 0.0, 2 * 2 * 256 * 9000), (200, 20001, 776, 1.0, 0),
+])
+def test_few_positions_and_a_large_head(dg, n, V, d, ignored, scratch):
+    """dW by the kernel that keeps the positions' hidden states, just under and over its limits; both types,
+    stored and added."""
+    h, W, y, dl = inputs(n, V, d, seed=n, ignored=ignored)
+    got = run(dg, h, W, y, dl, scratch_bytes=scratch)
+    if ignored < 1:
+        check(h, W, y, dl, 1.0, got)
+    assert ignored < 1 or all((x == 0).all() for x in got)
+    full = run(dg, h, W, y, dl, dw=torch.full(W.shape, 7.0, device="cuda"), scratch_bytes=scratch)[3]
+    assert np.array_equal(torch.from_numpy(full).float().bfloat16().double().numpy(), got[3])
+    added = run(dg, h, W, y, dl, dw=torch.ones(W.shape, device="cuda"), scratch_bytes=scratch, dw_accumulate=1)[3]
+    assert np.array_equal(added, (torch.from_numpy(full).float() + 1).double().numpy())
+    half = run(dg, h, W, y, dl, dw=torch.ones(W.shape, dtype=torch.bfloat16, device="cuda"), scratch_bytes=scratch,
+               dw_accumulate=1)[3]
+    assert np.array_equal(half, (torch.from_numpy(full).float() + 1).bfloat16().double().numpy())
+
+
+@pytest.mark.parametrize("n", [16384, 16385, 70001])
+def test_many_positions(dg, n):
+    """Past the sizes from which a CTA of the gather looks at more rows than 8."""
+    h, W, y, dl = inputs(n, 300, 16, seed=4, ignored=0.37)
+    check(h, W, y, dl, 1.0, run(dg, h, W, y, dl))
+
+
 def test_confident_positions_keep_their_digits(dg):
     """Losses down to 1e-10: the loss and the gradient's dominant term keep their relative precision."""
     h, W, y, dl = inputs(64, 512, 256, seed=5, lean=60.0)
