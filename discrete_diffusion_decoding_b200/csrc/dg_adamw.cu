@@ -576,10 +576,10 @@ cudaError_t launch_types(const Args<kCap>& a, bool state8, bool master, int n_ct
 
 bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
-// Launch the tensors [begin, end) as one grid; returns the status.
+// Launch the tensors [begin, end) as one grid (none where all are empty).
 template <int kCap>
 dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors, int begin, int end,
-                       int blocks_per_warp, cudaStream_t s) {
+                       int blocks_per_warp, int* launches, cudaStream_t s) {
     Args<kCap> a;
     std::memset(&a, 0, sizeof(a));
     a.lr = p->lr;
@@ -644,7 +644,9 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
     else
         e = p->grad_type == DG_FP32 ? launch_types<__nv_bfloat16, float>(a, s8, master, n, s)
                                     : launch_types<__nv_bfloat16, __nv_bfloat16>(a, s8, master, n, s);
-    return e == cudaSuccess ? DG_OK : DG_ECUDA;
+    if (e != cudaSuccess) return DG_ECUDA;
+    ++*launches;
+    return DG_OK;
 }
 
 }  // namespace
@@ -715,10 +717,9 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     for (int begin = 0; begin < n_tensors;) {
         const int left = n_tensors - begin;
         const int end = begin + (left > kManyTensors ? kManyTensors : left);
-        const dg_status st = left <= kFewTensors ? launch_range<kFewTensors>(p, tensors, begin, end, bpw, s)
-                                                 : launch_range<kManyTensors>(p, tensors, begin, end, bpw, s);
+        const dg_status st = left <= kFewTensors ? launch_range<kFewTensors>(p, tensors, begin, end, bpw, &launches, s)
+                                                 : launch_range<kManyTensors>(p, tensors, begin, end, bpw, &launches, s);
         if (st != DG_OK) return st;
-        ++launches;
         begin = end;
     }
     set_last_launches(launches);

@@ -303,7 +303,10 @@ def test_captured_and_replayed_with_new_inputs(dg):
     loss, lse = torch.empty(300, device="cuda"), torch.empty(300, device="cuda")
     dh, dW = torch.empty_like(hd), torch.empty_like(Wd)
 
+    dlsrc = dld.clone()
+
     def calls():
+        dld.copy_(dlsrc)                 # a copy node before the first kernel
         dg.dg_xent_forward(p, hd, Wd, yd, loss, lse, ws)
         dg.dg_xent_backward(p, hd, Wd, yd, loss, lse, dld, dh, dW, ws)
 
@@ -317,7 +320,7 @@ def test_captured_and_replayed_with_new_inputs(dg):
     for seed, ignored in ((1, 0.0), (2, 0.6), (3, 1.0), (4, 0.1)):
         h, W, y, dl = inputs(300, 3000, 128, seed=seed, ignored=ignored)
         want = run(dg, h, W, y, dl)
-        for a, b in ((hd, h), (Wd, W), (yd, y), (dld, dl)):
+        for a, b in ((hd, h), (Wd, W), (yd, y), (dlsrc, dl)):
             a.copy_(b)
         g.replay()
         torch.cuda.synchronize()
