@@ -1133,7 +1133,9 @@ constexpr long long kScratchBytes = 400LL << 20;     // of G in the backward, wh
 
 dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     if (!p || p->n < 0 || p->vocab < 1 || p->hidden < 1) return DG_EINVAL;
-    if (!(p->temperature > 0.f) || !std::isfinite(p->temperature)) return DG_EINVAL;
+    // 1 / T in fp32 too: below 4e-39 it is infinite, and every difference of logits with it
+    if (!(p->temperature > 0.f) || !std::isfinite(p->temperature) || !std::isfinite(kLog2e / p->temperature))
+        return DG_EINVAL;
     if (p->target_type != DG_INT32 && p->target_type != DG_INT64) return DG_EINVAL;
     if (p->dw_type != DG_BF16 && p->dw_type != DG_FP32) return DG_EINVAL;
     if (p->dw_accumulate != 0 && p->dw_accumulate != 1) return DG_EINVAL;
@@ -1437,6 +1439,7 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     const size_t h_bytes = 2 * (static_cast<size_t>(p->n - 1) * (p->h_stride ? p->h_stride : p->hidden) + p->hidden);
     if (dh_dev && (overlap(dh_dev, dh_bytes, W_dev, w_bytes) || overlap(dh_dev, dh_bytes, h_dev, h_bytes)))
         return DG_EINVAL;
+    if (dh_dev && dW_dev && overlap(dh_dev, dh_bytes, dW_dev, dw_bytes)) return DG_EINVAL;
     if (workspace_bytes < q.total) return DG_ENOMEM;
     if (!gemm_attr_set()) return DG_ECUDA;
 

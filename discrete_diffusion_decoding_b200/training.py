@@ -38,6 +38,12 @@ def _tensor(fn, name, t, dtypes, shape, device):
                     f"expected dense {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}")
 
 
+def _refuse_capture(fn, instead):
+    """Calls that count on the host: a graph would repeat the counts of its capture."""
+    if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
+        _refuse(fn, f"the stream is being captured; capture {instead}")
+
+
 def _call(fn, device, stream, *args):
     """The library's entry point `fn` on `stream`, or the device's current stream, with the device made current."""
     if device.type != "cuda":
@@ -293,8 +299,9 @@ class AdamWTensors:
 
 def dg_adamw_step(p, tensors, stream=None):
     """One AdamW step of every tensor of an AdamWTensors list; p from adamw_params (p.step counts from 1)."""
-    p.param_type, p.grad_type, p.state_bits = tensors.param_type, tensors.grad_type, tensors.state_bits
-    _call("dg_adamw_step", tensors.device, stream, ctypes.byref(p), tensors.table, tensors.n_tensors)
+    q = DgAdamWParams.from_buffer_copy(p)     # p may be another thread's too, beside tensors of other types
+    q.param_type, q.grad_type, q.state_bits = tensors.param_type, tensors.grad_type, tensors.state_bits
+    _call("dg_adamw_step", tensors.device, stream, ctypes.byref(q), tensors.table, tensors.n_tensors)
 
 
 class AdamW:
@@ -302,8 +309,8 @@ class AdamW:
 
     bf16 parameters keep a 32-bit master copy (`master`) or are rounded at random without one; `weight_decay`
     is one value or one for each parameter.  Steps take the parameters' .grad, or the list given to step();
-    a parameter without a gradient is left as it is.  (A captured step repeats the count and the rate of its
-    capture: graphs take dg_adamw_step with step_dev and lr_dev instead.)
+    a parameter without a gradient is left as it is.  The step count lives on the host, so a step is not
+    captured into a graph: graphs take dg_adamw_step with step_dev and lr_dev.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,
@@ -339,6 +346,7 @@ class AdamW:
             _refuse("AdamW", "parameters must be float32 or bfloat16")
 
     def step(self, grads=None, grad_scale=1.0, stream=None):
+        _refuse_capture("AdamW.step", "dg_adamw_step with step_dev")
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             _refuse("AdamW.step", "grads has another length than params")
@@ -389,7 +397,8 @@ class HeadTrainer:
 
     accumulate(h, targets) adds the gradients of one batch and returns (loss, dh): the weighted mean loss as
     a device scalar and the hidden states' gradient, for a denoiser to go on with; update() applies AdamW;
-    step() does both.  serving() gives the head in the layout that dg_denoise_step reads.
+    step() does both.  They count batches and steps on the host and are not captured into graphs (capture
+    dg_xent_forward, dg_xent_backward and dg_adamw_step).  serving() gives the head in the layout that dg_denoise_step reads.
     """
 
     def __init__(self, W, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,
@@ -407,6 +416,7 @@ class HeadTrainer:
 
     def accumulate(self, h, targets, weight=None):
         """h [n, d] bf16, targets [n]; weight float32 [n] (1 where None): the loss is sum w loss / sum w."""
+        _refuse_capture("HeadTrainer.accumulate", "dg_xent_forward and dg_xent_backward")
         p = xent_params(targets.numel(), self.W.shape[0], self.W.shape[1], temperature=self.temperature,
                         ignore_index=self.ignore_index, dw_accumulate=int(self.batches > 0))
         if self._ws is None or self._ws.nbytes < xent_workspace_size(p):

@@ -377,8 +377,8 @@ enum { DG_INT32 = 0, DG_INT64 = 1 };
 
 /*
  * Cross entropy of a head W [vocab, hidden] at n positions.  Limits: n >= 0, vocab >= 1,
- * temperature > 0 and finite, scratch_bytes >= 0 (DG_EINVAL otherwise); hidden a multiple of 8 up to 65536,
- * n up to 2^22, vocab up to 2^28 (DG_EUNSUPPORTED otherwise).
+ * temperature > 0 and finite, its reciprocal too, scratch_bytes >= 0 (DG_EINVAL otherwise);
+ * hidden a multiple of 8 up to 65536, n up to 2^22, vocab up to 2^28 (DG_EUNSUPPORTED otherwise).
  */
 typedef struct {
     int n;                  /* positions */
@@ -428,7 +428,7 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
  *   dloss_dev: [n] float
  *   dh_dev:    [n, hidden] bf16, 16-byte aligned (NULL: not wanted)
  *   dW_dev:    [vocab, hidden] bf16 or fp32 (dw_type), 16-byte aligned (NULL: not wanted)
- * At least one of dh_dev and dW_dev (DG_EINVAL); neither may overlap W, nor dh h (DG_EINVAL).
+ * At least one of dh_dev and dW_dev (DG_EINVAL); neither may overlap W or the other, nor dh h (DG_EINVAL).
  * n = 0 zeroes dW unless dw_accumulate.  The results of equal calls are equal to the bit.
  * Launches: three and one for every piece (see scratch_bytes).
  * A wait that runs out makes both gradients NaN.

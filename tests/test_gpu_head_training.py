@@ -1,5 +1,7 @@
 """The head's training as it is used: loss, gradients, AdamW and the decode that reads the trained head."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -192,3 +194,45 @@ def test_optimizer_notices_moved_parameters(dg):
     opt.refresh_master()
     opt.step([torch.ones_like(q)])
     assert (q == 3.0).all()
+
+
+def test_steps_that_count_on_the_host_are_not_captured(dg):
+    """A graph would repeat the bias correction, the random bits and the choice to add to dW of its capture."""
+    W = torch.ones(64, 8, dtype=torch.bfloat16, device="cuda")
+    tr, opt = dg.HeadTrainer(W.clone()), dg.AdamW([W])
+    h, y = torch.ones(3, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    x = torch.zeros(4, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.add_(1)
+        for call in (lambda: tr.step(h, y), lambda: tr.accumulate(h, y), lambda: opt.step([W.clone()])):
+            with pytest.raises(dg.DgError, match="captured"):
+                call()
+    assert tr.batches == 0 and opt.steps == 0
+    tr.step(h, y)
+    assert tr.optimizer.steps == 1
+
+
+def test_params_shared_by_lists_of_two_types(dg):
+    """The types of a call are its tensors', also while another thread steps with the same params."""
+    p = dg.adamw_params(lr=0.5, step=1)
+    before = bytes(p)
+    sets = []
+    for dtype in (torch.float32, torch.bfloat16):
+        w = torch.zeros(5000, dtype=dtype, device="cuda")
+        m, v = (torch.zeros(5000, device="cuda") for _ in range(2))
+        sets.append((w, dg.AdamWTensors([w], [torch.ones_like(w)], [m], [v])))
+    threads = [threading.Thread(target=lambda t=t: [dg.dg_adamw_step(p, t) for _ in range(200)]) for _, t in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert bytes(p) == before
+    for w, t in sets:
+        one = torch.zeros_like(w)
+        alone = dg.AdamWTensors([one], [torch.ones_like(w)], [torch.zeros(5000, device="cuda")],
+                                [torch.zeros(5000, device="cuda")])
+        for _ in range(200):
+            dg.dg_adamw_step(p, alone)
+        assert torch.equal(w, one)

@@ -405,7 +405,10 @@ def test_refusals_on_the_device(dg):
     for grads in ((None, None), (hd, dW), (dh, Wd), (Wd[:20], dW), (dh.float(), dW), (dh, dW.half())):
         with pytest.raises(dg.DgError):
             dg.dg_xent_backward(p, hd, Wd, yd, loss, lse, dld, *grads, ws)
-    for k, v in (("temperature", 0.0), ("temperature", float("nan")), ("dw_accumulate", 2), ("hidden", 60), ("scratch_bytes", -1)):
+    flat = torch.empty(600 * 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(dg.DgError):      # dh inside dW
+        dg.dg_xent_backward(p, hd, Wd, yd, loss, lse, dld, flat[64:21 * 64].view(20, 64), flat.view(600, 64), ws)
+    for k, v in (("temperature", 0.0), ("temperature", float("nan")), ("temperature", 1e-42), ("dw_accumulate", 2), ("hidden", 60), ("scratch_bytes", -1)):
         q = dg.xent_params(20, 600, 64)
         setattr(q, k, v)
         with pytest.raises(dg.DgError):

@@ -186,6 +186,7 @@ def test_c_entry_points_refuse_bad_arguments_without_a_device(dg):
     p = dg.xent_params(4, 9, 8)
     for field, value, want in (("n", -1, DG_EINVAL), ("vocab", 0, DG_EINVAL), ("hidden", 0, DG_EINVAL),
                                ("temperature", 0.0, DG_EINVAL), ("temperature", float("inf"), DG_EINVAL),
+                               ("temperature", 1e-42, DG_EINVAL),
                                ("target_type", 2, DG_EINVAL), ("dw_type", 5, DG_EINVAL), ("dw_accumulate", -1, DG_EINVAL),
                                ("h_stride", 7, DG_EINVAL), ("hidden", 12, DG_EUNSUPPORTED),
                                ("hidden", 65544, DG_EUNSUPPORTED), ("n", (1 << 22) + 1, DG_EUNSUPPORTED),
