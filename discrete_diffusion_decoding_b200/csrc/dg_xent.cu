@@ -17,7 +17,7 @@
 // vocabulary] tiles whose epilogue keeps a (maximum, sum) per row and half tile, and a merge.
 // Backward: launch k computes G for piece k + 1 of the vocabulary (the same product, G written in
 // bf16, the operand type of the two products that read it: each entry is off by at most 2^-8 of
-// itself, as an output in bf16 is) and both gradients' tiles for piece k, so that the tails, the
+// itself, as an output in bf16 is; see kRestRows for the target's) and both gradients' tiles for piece k, so that the tails, the
 // memory-bound and the compute-bound tiles of the three overlap; dW is written once, dh is added in
 // fp32 to slabs that the last launch sums, rounds and scatters.
 //
@@ -59,6 +59,11 @@ constexpr int kEpiBytes = 4096;            // an epilogue warp's rows on their w
 constexpr int kSmemBytes = kBoxes * kOperand + 8 * kEpiBytes + 1024;
 constexpr int kSched = 2;                  // items in hand: the one in work and the next
 constexpr int kPackRows = 8;               // rows a CTA of the gather looks at together
+// The target's entry is most of a row of G, and its rounding moves all of dh and of that row of dW together.  dh
+// takes what it leaves out in fp32 in the last launch, from the target's row of W.  dW takes it where at most this
+// many positions count: they fill half of the one stage that its sums then have, and the other half holds the
+// same hidden states against a G of these remainders, at no further product.
+constexpr int kRestRows = kK / 2;
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -91,7 +96,8 @@ struct Packed {
     float* lse2;         // backward: lse in log2 units
     float* coef;         // backward: dloss / T
     float* tcoef;        // backward: the target's entry of G
-    __nv_bfloat16* h;    // [rounded up to 256 rows, d]; zeros up to a multiple of 64 rows
+    float* trest;        // and what its rounding to bf16 leaves out
+    __nv_bfloat16* h;    // [rounded up to 256 rows, d]; zeros up to a multiple of 64 rows (see kRestRows)
     uint32_t* tickets;   // one counter of items for each launch of products
     int n_tickets;
 };
@@ -122,6 +128,17 @@ __device__ __forceinline__ bool counts(const PackArgs& a, int i, long long& y) {
 
 __device__ __forceinline__ void zero_row(__nv_bfloat16* dst, int d, int lane) {
     for (int c = lane * 8; c < d; c += 256) *reinterpret_cast<uint4*>(dst + c) = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void copy_row(__nv_bfloat16* dst, const __nv_bfloat16* src, int d, int lane, bool vec) {
+    if (vec) {
+#pragma unroll 4
+        for (int c = lane * 8; c < d; c += 256)
+            *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(src + c));
+    } else {
+#pragma unroll 4
+        for (int c = lane; c < d; c += 32) dst[c] = __ldg(src + c);
+    }
 }
 
 __device__ __forceinline__ float dot8(const uint4& a, const uint4& b, float acc) {
@@ -180,7 +197,9 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
         before += __popc(kept);
         y = __shfl_sync(0xffffffffu, y, warp);
         // the rows behind the last one kept, up to a whole stage of the products that sum over positions
-        if (i >= all && i < (all + kK - 1) / kK * kK) zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
+        const bool twice = a.dloss && all <= kRestRows;
+        if (i >= all && i < (all + kK - 1) / kK * kK && !(twice && i >= kRestRows && i < kRestRows + all))
+            zero_row(a.out.h + static_cast<long long>(i) * a.d, a.d, lane);
         if (i >= a.n) continue;
         if (!(kept >> warp & 1u)) {
             if (lane == 0 && a.loss_out) {
@@ -193,14 +212,8 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
         const bool inside = y >= 0 && y < a.vocab;
         const __nv_bfloat16* src = a.h + static_cast<long long>(i) * a.h_stride;
         __nv_bfloat16* dst = a.out.h + static_cast<long long>(at) * a.d;
-        if (vec) {
-#pragma unroll 4
-            for (int c = lane * 8; c < a.d; c += 256)
-                *reinterpret_cast<uint4*>(dst + c) = __ldg(reinterpret_cast<const uint4*>(src + c));
-        } else {
-#pragma unroll 4
-            for (int c = lane; c < a.d; c += 32) dst[c] = __ldg(src + c);
-        }
+        copy_row(dst, src, a.d, lane, vec);
+        if (twice) copy_row(dst + static_cast<long long>(kRestRows) * a.d, src, a.d, lane, vec);
         float zt = 0.f;
         if (!a.dloss && inside) {
             // read back what this warp has just written: the same values, whatever h's alignment
@@ -217,8 +230,10 @@ __global__ void __launch_bounds__(256) dg_xent_pack_kernel(const PackArgs a) {
             a.out.target[at] = inside ? static_cast<int32_t>(y) : -1;
             if (a.dloss) {
                 const float c = inside ? a.dloss[i] * a.inv_t : NAN;
+                const float t = c * expm1f(-a.loss_in[i]);
                 a.out.coef[at] = c;
-                a.out.tcoef[at] = c * expm1f(-a.loss_in[i]);
+                a.out.tcoef[at] = t;
+                a.out.trest[at] = t - __bfloat162float(__float2bfloat16_rn(t));
                 a.out.lse2[at] = a.lse_in[i] * kLog2e;
             } else {
                 a.out.zt2[at] = zt * a.scale_log2;
@@ -456,7 +471,8 @@ __device__ __forceinline__ void loss_epilogue(const GemmArgs& a, int n0, uint32_
     a.part[(static_cast<long long>(i) * a.tiles_logits) * 2 + n0 / kHalf] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
 }
 
-// This row's half tile of logits -> its entries of G in bf16; rows and columns outside are 0.
+// This row's half tile of logits -> its entries of G in bf16; rows and columns outside are 0, but for the
+// remainders of at most kRestRows positions in the rows kRestRows behind theirs.
 __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint32_t (&r)[kHalf], int i, int rows,
                                                 uint32_t own, int lane) {
     // rows that no later product reads (dW's sums end with the stage of the last position) are not written
@@ -464,7 +480,9 @@ __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint3
     const bool live = i < rows;
     const int limit = a.vocab - a.v0_logits;
     const float coef = live ? a.pk.coef[i] : 0.f, lse2 = live ? a.pk.lse2[i] : 0.f;
-    const int off = live ? a.pk.target[i] - a.v0_logits - n0 : -1;
+    const bool rest = rows <= kRestRows && i >= kRestRows && i - kRestRows < rows;
+    const int of = rest ? i - kRestRows : i;
+    const int off = live || rest ? a.pk.target[of] - a.v0_logits - n0 : -1;
     if (i - lane < rows) {
 #pragma unroll
         for (int k = 0; k < kHalf; ++k)
@@ -479,7 +497,7 @@ __device__ __forceinline__ void logits_epilogue(const GemmArgs& a, int n0, uint3
         for (int k = 0; k < kHalf; ++k)
             if (n0 + k >= limit) r[k] = 0;
     }
-    const float tcoef = off >= 0 && off < kHalf ? a.pk.tcoef[i] : 0.f;
+    const float tcoef = off >= 0 && off < kHalf ? (rest ? a.pk.trest[of] : a.pk.tcoef[of]) : 0.f;
 #pragma unroll
     for (int c = 0; c < kHalf; c += 64)
         rows_bf16(own, lane, &r[c], &a.g_out, n0 + c, a.g_write * a.g_rows + i - lane, off - c, tcoef);
@@ -1088,9 +1106,11 @@ __global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const flo
     }
 }
 
-// dh rows: the slabs' sum in bf16 at the original positions.  After a wait that ran out both gradients are NaN.
+// dh rows: the slabs' sum and the target's remainder (see kRestRows) in bf16 at the original positions.  After a
+// wait that ran out both gradients are NaN.
 __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const float* slab, long long slab_stride,
-                                                             int splits, int d, __nv_bfloat16* dh, uint32_t* dw_words,
+                                                             int splits, int d, const __nv_bfloat16* W,
+                                                             __nv_bfloat16* dh, uint32_t* dw_words,
                                                              long long n_dw_words) {
     griddep_launch();
     griddep_wait();
@@ -1105,6 +1125,9 @@ __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const fl
     for (long long k = first; k < static_cast<long long>(rows) * vecs; k += step) {
         const int i = static_cast<int>(k / vecs), c = static_cast<int>(k % vecs) * 4;
         const float* src = slab + static_cast<long long>(i) * d + c;
+        const int y = pk.target[i];
+        const float t = pk.trest[i];
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(W + static_cast<long long>(max(y, 0)) * d + c));
         float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 16
         for (int s = 0; s < splits; ++s) {
@@ -1113,6 +1136,12 @@ __global__ void __launch_bounds__(256) dg_xent_finish_kernel(Packed pk, const fl
             x[1] += u.y;
             x[2] += u.z;
             x[3] += u.w;
+        }
+        if (y >= 0) {            // outside the vocabulary: NaN already
+            x[0] = fmaf(t, __uint_as_float(w.x << 16), x[0]);
+            x[1] = fmaf(t, __uint_as_float(w.x & 0xFFFF0000u), x[1]);
+            x[2] = fmaf(t, __uint_as_float(w.y << 16), x[2]);
+            x[3] = fmaf(t, __uint_as_float(w.y & 0xFFFF0000u), x[3]);
         }
         uint2 o = make_uint2(bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]));
         if (bad) o = make_uint2(0x7FFF7FFFu, 0x7FFF7FFFu);
@@ -1125,7 +1154,7 @@ struct XentPlan {
     int rows_alloc, v_tiles, d_tiles, pairs;
     int piece, pieces;       // columns per piece of the backward, and their number
     int splits, kb_per_split;
-    size_t err, row, target, lse2, coef, tcoef, zt2, h, tickets, part, g, slab, total;
+    size_t err, row, target, lse2, coef, tcoef, trest, zt2, h, tickets, part, g, slab, total;
 };
 
 constexpr int kMaxRows = 1 << 22;
@@ -1165,6 +1194,7 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
     q.lse2 = take(4 * n);
     q.coef = take(4 * n);
     q.tcoef = take(4 * n);
+    q.trest = take(4 * n);
     q.zt2 = take(4 * n);
     q.h = take(2 * n * p->hidden);
     if (!backward) {
@@ -1218,6 +1248,7 @@ Packed packed_of(const XentPlan& q, void* ws) {
     k.lse2 = at<float>(ws, q.lse2);
     k.coef = at<float>(ws, q.coef);
     k.tcoef = at<float>(ws, q.tcoef);
+    k.trest = at<float>(ws, q.trest);
     k.h = at<__nv_bfloat16>(ws, q.h);
     return k;
 }
@@ -1503,7 +1534,7 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     if (blocks > q.pairs * 16LL) blocks = q.pairs * 16LL;
     if (launch_next(dg_xent_finish_kernel, static_cast<int>(blocks), 256, 1, 0, s, ga.pk,
                     static_cast<const float*>(slab), static_cast<long long>(rows * d), q.splits, p->hidden,
-                    static_cast<__nv_bfloat16*>(dh_dev), static_cast<uint32_t*>(dW_dev),
+                    static_cast<const __nv_bfloat16*>(W_dev), static_cast<__nv_bfloat16*>(dh_dev), static_cast<uint32_t*>(dW_dev),
                     static_cast<long long>(dw_bytes / 4)) != cudaSuccess)
         return DG_ECUDA;
     const int launches = q.pieces + 2;
