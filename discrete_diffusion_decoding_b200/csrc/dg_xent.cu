@@ -1095,8 +1095,9 @@ __global__ void __launch_bounds__(256) dg_xent_merge_kernel(Packed pk, const flo
         for (int w = 1; w < 8; ++w) merge_into(m, l, of_warp[w].x, of_warp[w].y);
         const int at = pk.row[i];
         float value = NAN, total = NAN;
-        if (*pk.err == 0 && pk.target[i] >= 0) {
-            const float zt = pk.zt2[i];
+        const float zt = pk.zt2[i];
+        // a target's logit of +inf would make the loss 0 and its gradient vanish
+        if (*pk.err == 0 && pk.target[i] >= 0 && fabsf(zt) < INFINITY) {
             const float gap = l > 0.f || l != l ? (m - zt + log2f(l)) * kLn2 : -INFINITY;   // no other column: -inf
             value = fmaxf(gap, 0.f) + log1pf(expf(-fabsf(gap)));
             total = zt * kLn2 + value;

@@ -408,7 +408,8 @@ size_t dg_xent_workspace_size(const dg_xent_params* p, int backward);
  *   lse_i = ln sum_v e^{z[i,v]},  loss_i = lse_i - z[i, y_i]   (nats, fp32)
  * computed so that small losses keep their relative precision.  Ignored positions get
  * loss 0 and lse 0 and cost nothing; their hidden states may hold anything.  A target
- * outside [0, vocab) that is not ignore_index gives NaN, and so do logits that are not finite.
+ * outside [0, vocab) that is not ignore_index gives NaN, and so do a target's logit that is not
+ * finite and any logit that is NaN or +infinity (another column's of -infinity has no share).
  *   h_dev:       [n, hidden] bf16, rows h_stride apart (any alignment; 16 bytes is faster)
  *   W_dev:       [vocab, hidden] bf16, row-major, 16-byte aligned
  *   targets_dev: [n] int32 or int64

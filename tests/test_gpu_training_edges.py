@@ -61,3 +61,36 @@ def test_the_targets_entry_of_g_is_not_rounded_away(dg, n, V, d, kept, scratch):
     B = torch.from_numpy(G).bfloat16().double().numpy()
     assert np.any(np.abs(torch.from_numpy(B @ W64).bfloat16().double().numpy() - dh) > tol_h)
     assert kept > 32 or np.any(np.abs(B.T @ h64 - dW) > tol_w)
+
+
+# ------------------------------------------------------------------ logits that are not finite
+@pytest.mark.parametrize("n", [4, 40])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), "overflow"])
+def test_a_target_whose_logit_is_not_finite_gives_nan(dg, n, value):
+    """A diverged row of the head reports no perfect loss: NaN in loss, lse, dh and dW, not 0."""
+    V, d = 600, 64
+    g = torch.Generator().manual_seed(n)
+    W = (torch.randn(V, d, generator=g) * 0.05).bfloat16()
+    h = torch.randn(n, d, generator=g).bfloat16()
+    y = torch.randint(0, V, (n,), generator=g).int()
+    y[y == 17] = 18
+    y[2] = 17
+    keep = np.arange(n) != 2
+    if value == "overflow":               # only position 2 has this product
+        W[:, 5], h[:, 5] = 0, 0
+        W[17, 5], h[2, 5] = 1e30, 1e30
+    else:                                 # every position sees the infinity; it is the target's at position 2
+        W[17, 6], h[:, 6] = value, 1.0
+    loss, lse, dh, dW = run(dg, h, W, y, torch.ones(n))
+    assert np.isnan(loss[2]) and np.isnan(lse[2]) and np.isnan(dh[2]).all() and np.isnan(dW).all()
+    if value == "overflow":
+        assert np.isfinite(loss[keep]).all() and np.isfinite(dh[keep]).all()
+    elif value == float("inf"):
+        assert np.isnan(loss).all() and np.isnan(dh).all()
+    elif value == float("-inf"):
+        # elsewhere the column has no share: the loss is that of the head without it
+        h64, W64 = h.double().numpy()[keep], np.delete(W.double().numpy(), 17, 0)
+        y0 = np.where(y.numpy() > 17, y.numpy() - 1, y.numpy())[keep]
+        want, want_lse = xent.cross_entropy(h64, W64, y0)
+        dz = xent.bounds(h64, W64, y0, 1.0, np.zeros((n - 1, V - 1)), want, want_lse)[0]
+        assert np.all(np.abs(loss[keep] - want) <= 2 * dz + 2.0 ** -20 * want)
