@@ -579,7 +579,7 @@ bool misaligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_
 // Launch the tensors [begin, end) as one grid (none where all are empty).
 template <int kCap>
 dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors, int begin, int end,
-                       int blocks_per_warp, int* launches, cudaStream_t s) {
+                       int blocks_per_warp, bool master, int* launches, cudaStream_t s) {
     Args<kCap> a;
     std::memset(&a, 0, sizeof(a));
     a.lr = p->lr;
@@ -611,7 +611,6 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
     long long ctas = 0;
     const uintptr_t pa = p->param_type == DG_FP32 ? 32 : 16, ga = p->grad_type == DG_FP32 ? 32 : 16;
     const uintptr_t sa = p->state_bits == 8 ? 8 : 32;
-    bool master = false;
     for (int i = begin; i < end; ++i) {
         const dg_adamw_tensor& x = tensors[i];
         Tensor& t = a.t[i - begin];
@@ -628,7 +627,6 @@ dg_status launch_range(const dg_adamw_params* p, const dg_adamw_tensor* tensors,
                       : static_cast<float>(1.0 - p->lr * static_cast<double>(x.weight_decay));
         t.aligned = !(misaligned(x.param, pa) || misaligned(x.grad, ga) || misaligned(x.m, sa) ||
                       misaligned(x.v, sa) || misaligned(x.master, 32));
-        master = master || x.master;
         a.first_cta[i - begin] = static_cast<int>(ctas);
         ctas += (x.n + per_cta - 1) / per_cta;
         if (ctas > 0x7fffffffLL) return DG_EINVAL;   // over 2^42 elements
@@ -688,10 +686,12 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     const uintptr_t ss = p->state_bits == 8 ? 1 : 4;
     long long total = 0;
     int with_master = 0, live = 0;
+    bool any_master = false;
     for (int i = 0; i < n_tensors; ++i) {
         const dg_adamw_tensor& x = tensors[i];
         if (x.n < 0 || x.n >= (1LL << 34)) return DG_EINVAL;     // element / 4 is one counter word
         if (!std::isfinite(x.weight_decay)) return DG_EINVAL;
+        any_master = any_master || x.master;
         if (x.n == 0) continue;
         if (!x.param || !x.grad || !x.m || !x.v) return DG_EINVAL;
         if (p->state_bits == 8 && (!x.m_exp || !x.v_exp)) return DG_EINVAL;
@@ -702,8 +702,9 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
         ++live;
         with_master += x.master != nullptr;
     }
-    // a master copy for all tensors of a call or for none, and only beside bf16 parameters that it rounds to
-    if (with_master != 0 && (with_master != live || p->param_type != DG_BF16 || p->stochastic)) return DG_EINVAL;
+    // a master copy for all tensors of a call or for none, and only beside bf16 parameters that it rounds to (an
+    // empty tensor needs none, but one that names it speaks for the call)
+    if (any_master && (with_master != live || p->param_type != DG_BF16 || p->stochastic)) return DG_EINVAL;
     // 8-bit states of many elements: 8 blocks a warp, which share the search of the list, the constants and the
     // exponents' accesses (262144 x 2816 bf16 parameters: 1.86 ms with 8, 1.92 with 4, 2.25 with 1).  fp32 states
     // (bound by the bytes; 65536 x 2816 with master: 0.751 ms with 1, 0.799 with 8) and few elements (to spread
@@ -717,8 +718,9 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     for (int begin = 0; begin < n_tensors;) {
         const int left = n_tensors - begin;
         const int end = begin + (left > kManyTensors ? kManyTensors : left);
-        const dg_status st = left <= kFewTensors ? launch_range<kFewTensors>(p, tensors, begin, end, bpw, &launches, s)
-                                                 : launch_range<kManyTensors>(p, tensors, begin, end, bpw, &launches, s);
+        const dg_status st =
+            left <= kFewTensors ? launch_range<kFewTensors>(p, tensors, begin, end, bpw, any_master, &launches, s)
+                                : launch_range<kManyTensors>(p, tensors, begin, end, bpw, any_master, &launches, s);
         if (st != DG_OK) return st;
         begin = end;
     }

@@ -482,7 +482,8 @@ typedef struct {
     void* v;
     int8_t* m_exp;          /* [ceil(n / 256)], state_bits 8 only */
     int8_t* v_exp;
-    float* master;          /* [n] fp32 or NULL: for all tensors of a call or for none */
+    float* master;          /* [n] fp32, or NULL in every tensor of the call: where any tensor names
+                             * one, an empty one too, all that have elements do */
     long long n;            /* 0 <= n < 2^34 */
     float weight_decay;
 } dg_adamw_tensor;

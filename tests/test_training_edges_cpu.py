@@ -1,0 +1,30 @@
+"""Refusals of the training entry points at the edges of what they document, without a GPU."""
+
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def dg():
+    from discrete_diffusion_decoding_b200 import build
+    build.build()
+    import discrete_diffusion_decoding_b200 as m
+    return m
+
+
+@pytest.mark.parametrize("order", [(0, 1), (1, 0)])
+@pytest.mark.parametrize("count", [2, 30, 500])
+def test_a_master_of_an_empty_tensor_asks_for_the_others(dg, order, count):
+    """An empty tensor's master among tensors without one: refused like the mixture of tensors with elements, before
+    the device is looked at."""
+    from discrete_diffusion_decoding_b200._abi import DG_EINVAL, DgAdamWTensor, lib
+    a = 1 << 20                               # never dereferenced
+    p = dg.adamw_params(param_type=1, grad_type=1)
+    empty = dict(param=a, grad=a, m=a, v=a, master=a, n=0)
+    plain = dict(param=a, grad=a, m=a, v=a, n=8)
+    table = (DgAdamWTensor * count)(*[DgAdamWTensor(**plain)] * count)
+    for place, at in zip((empty, plain), (0, count - 1) if order == (0, 1) else (count - 1, 0)):
+        table[at] = DgAdamWTensor(**place)
+    assert lib().dg_adamw_step(ctypes.byref(p), table, count, None) == DG_EINVAL
