@@ -299,6 +299,10 @@ class AdamWTensors:
 
 def dg_adamw_step(p, tensors, stream=None):
     """One AdamW step of every tensor of an AdamWTensors list; p from adamw_params (p.step counts from 1)."""
+    for t in getattr(p, "held", ()):
+        if t.device != tensors.device:
+            _refuse("dg_adamw_step", f"lr_dev, step_dev and grad_scale_dev lie where the tensors do, on "
+                                     f"{tensors.device}, not on {t.device}")
     q = DgAdamWParams.from_buffer_copy(p)     # p may be another thread's too, beside tensors of other types
     q.param_type, q.grad_type, q.state_bits = tensors.param_type, tensors.grad_type, tensors.state_bits
     _call("dg_adamw_step", tensors.device, stream, ctypes.byref(q), tensors.table, tensors.n_tensors)

@@ -28,3 +28,14 @@ def test_a_master_of_an_empty_tensor_asks_for_the_others(dg, order, count):
     for place, at in zip((empty, plain), (0, count - 1) if order == (0, 1) else (count - 1, 0)):
         table[at] = DgAdamWTensor(**place)
     assert lib().dg_adamw_step(ctypes.byref(p), table, count, None) == DG_EINVAL
+
+
+def test_scalars_of_another_device_are_refused(dg):
+    """The kernel reads them, so they lie where the tensors do."""
+    z = [torch.zeros(5) for _ in range(4)]
+    T = dg.AdamWTensors(z[:1], z[1:2], z[2:3], z[3:])
+    T.device = torch.device("cuda", 0)
+    p = dg.adamw_params()
+    p.held = [torch.zeros(1, device="meta")]          # stands for a second CUDA device's
+    with pytest.raises(dg.DgError, match="lr_dev, step_dev and grad_scale_dev"):
+        dg.dg_adamw_step(p, T)
