@@ -364,8 +364,27 @@ struct Lane {
             for (int j = 0; j < 2; ++j) {
                 mx[2 * i + j] = __fadd_rn(x[j], y[j]);
                 vx[2 * i + j] = __fadd_rn(u[j], w[j]);
-                r[2 * i + j] = sqrt_sfu(vx[2 * i + j]);
             }
+        }
+        // The flushing SFU root, which takes a subnormal for 0.  Lanes that hold one (gradients of about 1e-18), or
+        // a 0, scale it into the normal range first; the roots themselves are normal.  262144 x 2816 bf16 parameters
+        // with 8-bit states: 1.91 ms without this, 1.92 with it, 1.94 with the root that keeps subnormals everywhere.
+        float least = vx[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) least = fminf(least, vx[i]);
+        if (least < 0x1p-126f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool tiny = vx[i] < 0x1p-126f;
+                r[i] = sqrt_sfu(tiny ? vx[i] * 0x1p64f : vx[i]) * (tiny ? 0x1p-32f : 1.f);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = sqrt_sfu(vx[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x[2], y[2];
             unpack2(mul2(pack2(mx[2 * i], mx[2 * i + 1]), rate), x[0], x[1]);
             unpack2(fma2(pack2(r[2 * i], r[2 * i + 1]), bias, eps), y[0], y[1]);
             unpack2(fma2(pack2(px[2 * i], px[2 * i + 1]), keep, pack2(div_sfu(x[0], y[0]), div_sfu(x[1], y[1]))),

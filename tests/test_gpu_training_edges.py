@@ -5,7 +5,8 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import xent
+from oracle import adamw, xent
+from test_gpu_adamw import check_roots
 from test_gpu_xent import IGNORE, run
 
 pytestmark = pytest.mark.gpu
@@ -94,3 +95,41 @@ def test_a_target_whose_logit_is_not_finite_gives_nan(dg, n, value):
         want, want_lse = xent.cross_entropy(h64, W64, y0)
         dz = xent.bounds(h64, W64, y0, 1.0, np.zeros((n - 1, V - 1)), want, want_lse)[0]
         assert np.all(np.abs(loss[keep] - want) <= 2 * dz + 2.0 ** -20 * want)
+
+
+# ------------------------------------------------------------------ values below the normal range
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("eps", [0.0, 1e-8])
+def test_roots_of_subnormal_second_moments(dg, bits, eps):
+    """Gradients of 1e-19: v is positive but below the normal range.  Its root is normal, and is what the step
+    divides by and what an 8-bit state holds."""
+    n = 512
+    g = torch.linspace(1.5e-19, 1e-18, n)
+    g[300:] = 1e-3
+    g[0] = 0
+    p = torch.zeros(n)
+    p[0] = 1.0
+    dev = {k: torch.zeros(n, dtype=torch.uint8 if bits == 8 else torch.float32, device="cuda") for k in "mv"}
+    ex = {k: torch.zeros(2, dtype=torch.int8, device="cuda") for k in "mv"}
+    pd = p.cuda()
+    # element 0 has no moments: with eps 0 the definition divides 0 by 0
+    T = dg.AdamWTensors([pd], [g.cuda()], [dev["m"]], [dev["v"]], m_exp=[ex["m"]] if bits == 8 else None,
+                        v_exp=[ex["v"]] if bits == 8 else None)
+    dg.dg_adamw_step(dg.adamw_params(lr=1e-2, beta1=0.9, beta2=0.99, eps=eps, step=1, seed=4), T)
+    m, v = adamw.moments(g.numpy(), np.zeros(n), np.zeros(n), 0.9, 0.99)
+    assert 0 < v[1] < 2.0 ** -126 and v[299] < 2.0 ** -126 < v[300]
+    with np.errstate(invalid="ignore"):
+        want = -1e-2 * (m.astype(np.float64) / (1 - 0.9)) / (np.sqrt(v.astype(np.float64) / (1 - 0.99)) + eps)
+    got = pd.cpu().double().numpy()
+    assert np.isnan(got[0]) if eps == 0 else got[0] == 1
+    # root 3 u, its product and the sum 3 u, the rate and the numerator 3 u, the quotient 4 u, the sum u
+    assert np.all(np.abs(got - want)[1:] <= 16 * 2.0 ** -24 * np.abs(want[1:]))
+    if bits == 32:
+        assert np.array_equal(dev["m"].cpu().numpy(), m) and np.array_equal(dev["v"].cpu().numpy(), v)
+        return
+    um, uv = adamw.random_halves(4, n, 1, 0)
+    cm, em = adamw.encode(m, um)
+    assert np.array_equal(dev["m"].cpu().numpy(), cm) and np.array_equal(ex["m"].cpu().numpy(), em)
+    check_roots(dev["v"], ex["v"], v, uv)
+    root = adamw.decode(dev["v"].cpu().numpy(), ex["v"].cpu().numpy())
+    assert np.all(np.abs(root[1:256] / np.sqrt(v[1:256].astype(np.float64)) - 1) <= 0.125)
