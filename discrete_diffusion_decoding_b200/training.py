@@ -419,7 +419,8 @@ class HeadTrainer:
         self._ws = None           # the workspace of the largest batch so far
 
     def accumulate(self, h, targets, weight=None):
-        """h [n, d] bf16, targets [n]; weight float32 [n] (1 where None): the loss is sum w loss / sum w."""
+        """h [n, d] bf16, targets [n]; weight float32 [n] (1 where None): the loss is sum w loss / sum w over the
+        positions whose target counts; elsewhere the weight may hold anything."""
         _refuse_capture("HeadTrainer.accumulate", "dg_xent_forward and dg_xent_backward")
         p = xent_params(targets.numel(), self.W.shape[0], self.W.shape[1], temperature=self.temperature,
                         ignore_index=self.ignore_index, dw_accumulate=int(self.batches > 0))
@@ -428,9 +429,8 @@ class HeadTrainer:
         loss = torch.empty(p.n, dtype=torch.float32, device=self.W.device)
         lse = torch.empty_like(loss)
         dg_xent_forward(p, h, self.W, targets, loss, lse, self._ws)
-        w = (targets != self.ignore_index).float()
-        if weight is not None:
-            w = w * weight
+        kept = targets != self.ignore_index
+        w = kept.float() if weight is None else torch.where(kept, weight, 0.0).float()
         dloss = w / w.sum().clamp(min=torch.finfo(torch.float32).tiny)
         dh = torch.empty((p.n, p.hidden), dtype=torch.bfloat16, device=self.W.device)
         dg_xent_backward(p, h, self.W, targets, loss, lse, dloss, dh, self.dW, self._ws)

@@ -7,7 +7,7 @@ import torch
 
 from oracle import adamw, xent
 from test_gpu_adamw import check_roots
-from test_gpu_xent import IGNORE, run
+from test_gpu_xent import IGNORE, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -133,3 +133,18 @@ def test_roots_of_subnormal_second_moments(dg, bits, eps):
     check_roots(dev["v"], ex["v"], v, uv)
     root = adamw.decode(dev["v"].cpu().numpy(), ex["v"].cpu().numpy())
     assert np.all(np.abs(root[1:256] / np.sqrt(v[1:256].astype(np.float64)) - 1) <= 0.125)
+
+
+# ------------------------------------------------------------------ the trainer's weights
+@pytest.mark.parametrize("junk", [float("inf"), float("nan"), -float("inf")])
+def test_weights_of_ignored_positions_may_hold_anything(dg, junk):
+    V, d, n = 300, 64, 50
+    h, W, y, w = inputs(n, V, d, seed=1, ignored=0.4)
+    bad = torch.where(y == IGNORE, torch.tensor(junk), w)
+    out = []
+    for weight in (torch.where(y == IGNORE, 0.0, w), bad):
+        tr = dg.HeadTrainer(W.cuda().clone())
+        loss, dh = tr.accumulate(h.cuda(), y.cuda(), weight.cuda())
+        out.append((loss, dh, tr.dW))
+    for a, b in zip(*out):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
