@@ -431,7 +431,7 @@ class HeadTrainer:
         dg_xent_forward(p, h, self.W, targets, loss, lse, self._ws)
         kept = targets != self.ignore_index
         w = kept.float() if weight is None else torch.where(kept, weight, 0.0).float()
-        dloss = w / w.sum().clamp(min=torch.finfo(torch.float32).tiny)
+        dloss = torch.where(w != 0, w / w.sum(), 0)         # 0 also where nothing counts
         dh = torch.empty((p.n, p.hidden), dtype=torch.bfloat16, device=self.W.device)
         dg_xent_backward(p, h, self.W, targets, loss, lse, dloss, dh, self.dW, self._ws)
         self.batches += 1

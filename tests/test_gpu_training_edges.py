@@ -148,3 +148,16 @@ def test_weights_of_ignored_positions_may_hold_anything(dg, junk):
         out.append((loss, dh, tr.dW))
     for a, b in zip(*out):
         assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_weights_of_either_sign(dg):
+    """The loss is sum w loss / sum w also where the weights' sum is negative; without any weight it is 0."""
+    V, d, n = 300, 64, 50
+    h, W, y, w = inputs(n, V, d, seed=2, ignored=0.2)
+    out = []
+    for weight in (w, -w, w * 0):
+        tr = dg.HeadTrainer(W.cuda().clone())
+        loss, dh = tr.accumulate(h.cuda(), y.cuda(), weight.cuda())
+        out.append((loss, dh, tr.dW))
+    for a, b, c in zip(*out):
+        assert torch.equal(a, b) and (c == 0).all()
