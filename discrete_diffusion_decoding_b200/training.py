@@ -13,8 +13,11 @@ import torch
 from . import _abi
 from ._abi import DgAdamWParams, DgAdamWTensor, DgError, DgXentParams, check, lib
 
-# the handle of a device's current stream (torch.cuda.current_stream builds an object around it: 2 us)
+# what the public forms of these do with a few microseconds of checks and objects around it: the handle of a device's
+# current stream, the current device, and a count of a write in each of a list of tensors
 _current_stream = torch._C._cuda_getCurrentRawStream
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_count_writes = torch._C._increment_version
 
 _TYPES = {torch.float32: _abi.DG_FP32, torch.bfloat16: _abi.DG_BF16}
 _INDEX = {torch.int32: _abi.DG_INT32, torch.int64: _abi.DG_INT64}
@@ -44,21 +47,27 @@ def _refuse_capture(fn, instead):
         _refuse(fn, f"the stream is being captured; capture {instead}")
 
 
-def _call(fn, device, stream, *args):
-    """The library's entry point `fn` on `stream`, or the device's current stream, with the device made current."""
-    if device.type != "cuda":
+def _call(fn, device, stream, written, *args):
+    """The library's entry point `fn` on `stream`, or the device's current stream, with the device made current.
+
+    The tensors `written` count a write as torch's own in-place operations do, so that a backward which saved one
+    of them refuses (a replay of a captured call is not counted).
+    """
+    index = device.index
+    if index is None:             # host and meta tensors have none
         _refuse(fn, f"tensors are on {device}, expected a CUDA device")
     if stream is None:
-        handle = _current_stream(device.index)
+        handle = _current_stream(index)
     elif stream.device != device:
         _refuse(fn, f"the stream is on {stream.device}, the tensors on {device}")
     else:
         handle = stream.cuda_stream
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == index:
         check(fn, getattr(lib(), fn)(*args, handle))
     else:
         with torch.cuda.device(device):
             check(fn, getattr(lib(), fn)(*args, handle))
+    _count_writes(written)
 
 
 _DEFAULTS = {}
@@ -135,8 +144,8 @@ def dg_xent_forward(p, h, W, targets, loss, lse, ws, stream=None):
     _tensor(fn, "loss", loss, (torch.float32,), (p.n,), dev)
     if lse is not None:
         _tensor(fn, "lse", lse, (torch.float32,), (p.n,), dev)
-    _call(fn, dev, stream, ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(ws.buf),
-          ws.nbytes)
+    _call(fn, dev, stream, (loss,) if lse is None else (loss, lse), ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets),
+          _ptr(loss), _ptr(lse), _ptr(ws.buf), ws.nbytes)
 
 
 def dg_xent_backward(p, h, W, targets, loss, lse, dloss, dh, dW, ws, stream=None):
@@ -153,8 +162,8 @@ def dg_xent_backward(p, h, W, targets, loss, lse, dloss, dh, dW, ws, stream=None
     if dW is not None:
         _tensor(fn, "dW", dW, (torch.bfloat16, torch.float32), (p.vocab, p.hidden), dev)
         q.dw_type = _TYPES[dW.dtype]
-    _call(fn, dev, stream, ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets), _ptr(loss), _ptr(lse), _ptr(dloss),
-          _ptr(dh), _ptr(dW), _ptr(ws.buf), ws.nbytes)
+    _call(fn, dev, stream, [t for t in (dh, dW) if t is not None], ctypes.byref(q), _ptr(h), _ptr(W), _ptr(targets),
+          _ptr(loss), _ptr(lse), _ptr(dloss), _ptr(dh), _ptr(dW), _ptr(ws.buf), ws.nbytes)
 
 
 class _HeadCrossEntropy(torch.autograd.Function):
@@ -295,6 +304,8 @@ class AdamWTensors:
             row.n = 0 if g is None else p.numel()
         self.grad_type = _TYPES[gtype or torch.float32]
         self.grads = grads
+        # what a step writes and autograd may have saved
+        self.updated = [p for part in (self.params, self.master) if part for p, g in zip(part, grads) if g is not None]
 
 
 def dg_adamw_step(p, tensors, stream=None):
@@ -305,7 +316,7 @@ def dg_adamw_step(p, tensors, stream=None):
                                      f"{tensors.device}, not on {t.device}")
     q = DgAdamWParams.from_buffer_copy(p)     # p may be another thread's too, beside tensors of other types
     q.param_type, q.grad_type, q.state_bits = tensors.param_type, tensors.grad_type, tensors.state_bits
-    _call("dg_adamw_step", tensors.device, stream, ctypes.byref(q), tensors.table, tensors.n_tensors)
+    _call("dg_adamw_step", tensors.device, stream, tensors.updated, ctypes.byref(q), tensors.table, tensors.n_tensors)
 
 
 class AdamW:

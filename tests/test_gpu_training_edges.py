@@ -161,3 +161,42 @@ def test_weights_of_either_sign(dg):
         out.append((loss, dh, tr.dW))
     for a, b, c in zip(*out):
         assert torch.equal(a, b) and (c == 0).all()
+
+
+# ------------------------------------------------------------------ autograd and the optimizer
+@pytest.mark.parametrize("update", ["AdamW", "HeadTrainer", "dg_adamw_step"])
+def test_a_backward_after_the_weights_changed_is_refused(dg, update):
+    W = torch.randn(100, 64, device="cuda").bfloat16().requires_grad_()
+    h = torch.randn(5, 64, device="cuda").bfloat16().requires_grad_()
+    y = torch.arange(5, device="cuda")
+    loss = dg.head_cross_entropy(h, W, y).sum()
+    if update == "AdamW":
+        dg.AdamW([W]).step([torch.ones_like(W)])
+    elif update == "HeadTrainer":
+        dg.HeadTrainer(W).step(h.detach(), y)
+    else:
+        m, v = torch.zeros(100, 64, device="cuda"), torch.zeros(100, 64, device="cuda")
+        dg.dg_adamw_step(dg.adamw_params(), dg.AdamWTensors([W], [torch.ones_like(W)], [m], [v]))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_tensors_that_the_entry_points_write_count_it(dg):
+    h, W, y, dl = (x.cuda() for x in inputs(20, 300, 64))
+    p = dg.xent_params(20, 300, 64)
+    ws = dg.XentWorkspace(p)
+    loss, lse = torch.zeros(20, device="cuda"), torch.zeros(20, device="cuda")
+    dh, dW = torch.zeros_like(h), torch.zeros_like(W)
+    seen = [x._version for x in (loss, lse, dh, dW)]
+    dg.dg_xent_forward(p, h, W, y, loss, lse, ws)
+    dg.dg_xent_backward(p, h, W, y, loss, lse, dl, dh, dW, ws)
+    assert all(x._version > v for x, v in zip((loss, lse, dh, dW), seen))
+    assert h._version == 0 and W._version == 0
+    # a parameter without a gradient is not written
+    q = [torch.zeros(5, device="cuda"), torch.zeros(5, device="cuda")]
+    dg.AdamW(q, state_bits=32).step([torch.ones(5, device="cuda"), None])
+    assert q[0]._version == 1 and q[1]._version == 0
+    with torch.inference_mode():
+        r = torch.zeros(5, device="cuda")
+    dg.AdamW([r], state_bits=32).step([torch.ones(5, device="cuda")])
+    assert (r < 0).all()
