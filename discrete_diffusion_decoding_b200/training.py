@@ -233,8 +233,9 @@ class AdamWTensors:
     """The list of tensors of dg_adamw_step: parameters, gradients, states, and optionally 32-bit masters.
 
     m and v are float32 like the parameters, or uint8 codes beside m_exp and v_exp (int8, one for every 256
-    elements).  `grads` may hold None for a tensor to leave out; set_grads renews them.  The tensors are held
-    by this list; memory that is written must not overlap.
+    elements); gradients and states have their parameter's shape or are flat.  `grads` may hold None for a tensor
+    to leave out; set_grads renews them.  The tensors are held by this list; memory that is written must not
+    overlap.
     """
 
     def __init__(self, params, grads, m, v, m_exp=None, v_exp=None, master=None, weight_decay=0.0):
@@ -274,7 +275,8 @@ class AdamWTensors:
                     _tensor(fn, f"{name} {i}", t, (torch.int8,), (-(-n // BLOCK),), self.device)
                 else:
                     dtype = torch.float32 if name == "master" else state
-                    _tensor(fn, f"{name} {i}", t, (dtype,), t.shape if t.numel() == n else p.shape, self.device)
+                    # as the parameter, or flat
+                    _tensor(fn, f"{name} {i}", t, (dtype,), t.shape if t.shape == (n,) else p.shape, self.device)
                 setattr(row, name, _ptr(t))
                 spans.append((t.data_ptr(), t.numel() * t.element_size()))
         spans = sorted(s for s in spans if s[1])
@@ -296,9 +298,11 @@ class AdamWTensors:
                 gtype = g.dtype
                 if gtype not in _TYPES:
                     _refuse(fn, f"gradients are {gtype}, expected float32 or bfloat16")
-            if g.dtype != gtype or g.device != self.device or g.numel() != p.numel() or not g.is_contiguous():
+            if (g.dtype != gtype or g.device != self.device or not g.is_contiguous() or
+                    g.shape != p.shape and g.shape != (p.numel(),)):
                 _refuse(fn, f"gradient {g.dtype} {tuple(g.shape)} on {g.device} of a parameter {tuple(p.shape)}: "
-                            "expected dense gradients of one type on the parameters' device")
+                            "expected dense gradients of one type, in their parameters' shapes or flat, on their "
+                            "device")
         for row, g, p in zip(self.table, grads, self.params):
             row.grad = None if g is None else g.data_ptr()
             row.n = 0 if g is None else p.numel()

@@ -39,3 +39,24 @@ def test_scalars_of_another_device_are_refused(dg):
     p.held = [torch.zeros(1, device="meta")]          # stands for a second CUDA device's
     with pytest.raises(dg.DgError, match="lr_dev, step_dev and grad_scale_dev"):
         dg.dg_adamw_step(p, T)
+
+
+def test_gradients_and_states_have_their_parameters_shape(dg):
+    """A [6, 4] gradient of a [4, 6] parameter is another parameter's; flat ones are read in its order."""
+    def z(*shape):
+        return torch.zeros(shape)
+
+    for grad in (z(6, 4), z(24, 1), z(1, 4, 6)):
+        with pytest.raises(dg.DgError):
+            dg.AdamWTensors([z(4, 6)], [grad], [z(4, 6)], [z(4, 6)])
+        T = dg.AdamWTensors([z(4, 6)], [None], [z(4, 6)], [z(24)])
+        with pytest.raises(dg.DgError):
+            T.set_grads([grad])
+        assert T.table[0].n == 0
+    opt = dg.AdamW([z(4, 6), z(6, 4)], state_bits=32)
+    with pytest.raises(dg.DgError):
+        opt.step([z(6, 4), z(4, 6)])
+    assert opt.steps == 0
+    with pytest.raises(dg.DgError):
+        dg.AdamWTensors([z(4, 6)], [z(4, 6)], [z(6, 4)], [z(4, 6)])
+    assert dg.AdamWTensors([z(4, 6)], [z(24)], [z(24)], [z(24)]).table[0].n == 24
