@@ -312,8 +312,15 @@ class AdamWTensors:
         self.updated = [p for part in (self.params, self.master) if part for p, g in zip(part, grads) if g is not None]
 
 
+    def release_grads(self):
+        """Drop the gradients; the next step needs set_grads first."""
+        self.grads = None
+
+
 def dg_adamw_step(p, tensors, stream=None):
     """One AdamW step of every tensor of an AdamWTensors list; p from adamw_params (p.step counts from 1)."""
+    if tensors.grads is None:
+        _refuse("dg_adamw_step", "the list's gradients were released: call set_grads first")
     for t in getattr(p, "held", ()):
         if t.device != tensors.device:
             _refuse("dg_adamw_step", f"lr_dev, step_dev and grad_scale_dev lie where the tensors do, on "
@@ -328,7 +335,7 @@ class AdamW:
 
     bf16 parameters keep a 32-bit master copy (`master`) or are rounded at random without one; `weight_decay`
     is one value or one for each parameter.  Steps take the parameters' .grad, or the list given to step();
-    a parameter without a gradient is left as it is.  The step count lives on the host, so a step is not
+    a parameter without a gradient is left as it is.  No gradient is held after the step.  The step count lives on the host, so a step is not
     captured into a graph: graphs take dg_adamw_step with step_dev and lr_dev.
     """
 
@@ -373,14 +380,24 @@ class AdamW:
             for i, row in zip(at, tensors.table):
                 if self.params[i].data_ptr() != (row.param or 0):
                     _refuse("AdamW.step", f"parameter {i} lies elsewhere than when the optimizer was made")
-            tensors.set_grads([grads[i] for i in at])
-        for k, (_, tensors) in enumerate(self.groups):
-            plain_bf16 = tensors.param_type == _abi.DG_BF16 and not tensors.table[0].master
-            # a key of its own for each list, whose tensors count from 0
-            p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps, step=self.steps + 1,
-                             grad_scale=grad_scale, seed=(self.seed + (k << 63)) & (1 << 64) - 1,
-                             stochastic=int(plain_bf16))
-            dg_adamw_step(p, tensors, stream)
+        try:
+            for at, tensors in self.groups:
+                tensors.set_grads([grads[i] for i in at])
+            for k, (_, tensors) in enumerate(self.groups):
+                plain_bf16 = tensors.param_type == _abi.DG_BF16 and not tensors.table[0].master
+                # a key of its own for each list, whose tensors count from 0
+                p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps,
+                                 step=self.steps + 1, grad_scale=grad_scale,
+                                 seed=(self.seed + (k << 63)) & (1 << 64) - 1, stochastic=int(plain_bf16))
+                dg_adamw_step(p, tensors, stream)
+        finally:
+            for _, tensors in self.groups:
+                tensors.release_grads()
+        if stream is not None:
+            # the caller may drop them too, while this stream still waits to read them
+            for g in grads:
+                if g is not None:
+                    g.record_stream(stream)
         self.steps += 1
 
     def refresh_master(self):

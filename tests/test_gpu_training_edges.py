@@ -1,6 +1,9 @@
 """The training entry points on the GPU where they could go wrong at the edges of what they document: rounding of
 the gradients' largest entries, logits that are not finite, values below the normal range, steps and streams."""
 
+import gc
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -200,3 +203,34 @@ def test_tensors_that_the_entry_points_write_count_it(dg):
         r = torch.zeros(5, device="cuda")
     dg.AdamW([r], state_bits=32).step([torch.ones(5, device="cuda")])
     assert (r < 0).all()
+
+
+def test_zero_grad_frees_the_gradients(dg):
+    p = torch.nn.Parameter(torch.zeros(1000, device="cuda"))
+    opt = dg.AdamW([p])
+    p.grad = torch.ones(1000, device="cuda")
+    held = weakref.ref(p.grad)
+    opt.step()
+    opt.zero_grad()
+    gc.collect()
+    assert held() is None
+    with pytest.raises(dg.DgError, match="gradients"):
+        dg.dg_adamw_step(dg.adamw_params(), opt.groups[0][1])
+
+
+def test_gradients_outlive_a_step_on_another_stream(dg):
+    """Gradients dropped after a step that still waits on its stream are not handed out again before it ran."""
+    n = 1 << 20
+    p = torch.zeros(n, device="cuda")
+    opt, side = dg.AdamW([p], lr=1.0, eps=0.0, state_bits=32), torch.cuda.Stream()
+    g = torch.ones(n, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)        # 0.1 s
+    opt.step([g], stream=side)
+    del g
+    opt.zero_grad()
+    other = [torch.full((n,), -1.0, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    # one step of a gradient of 1: m / (1 - b1) over the root of v / (1 - b2), each within 2^-20
+    assert ((p + 1).abs() <= 2.0 ** -19).all() and len(other) == 4
