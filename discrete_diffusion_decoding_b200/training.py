@@ -262,11 +262,14 @@ class AdamWTensors:
         self.params, self.master = params, lists.get("master")
         self.held = [params] + list(lists.values())
         self.table = (DgAdamWTensor * k)()
+        self.rows = list(self.table)          # views of it
+        self.shapes, self.sizes = [p.shape for p in params], [p.numel() for p in params]
+        self.at = [p.data_ptr() for p in params]
         spans = []
         for i, p in enumerate(params):
             _tensor(fn, f"parameter {i}", p, (ptype,), p.shape, self.device)
-            n = p.numel()
-            row = self.table[i]
+            n = self.sizes[i]
+            row = self.rows[i]
             row.param, row.n, row.weight_decay = _ptr(p), n, decay[i]
             spans.append((p.data_ptr(), n * p.element_size()))
             for name, x in lists.items():
@@ -291,25 +294,46 @@ class AdamWTensors:
         if len(grads) != self.n_tensors:
             _refuse(fn, "the lists differ in length")
         gtype = None
-        for g, p in zip(grads, self.params):
+        live = []                             # the places that a step takes
+        for k, g in enumerate(grads):
             if g is None:
                 continue
             if gtype is None:
                 gtype = g.dtype
                 if gtype not in _TYPES:
                     _refuse(fn, f"gradients are {gtype}, expected float32 or bfloat16")
+            shape = g.shape
             if (g.dtype != gtype or g.device != self.device or not g.is_contiguous() or
-                    g.shape != p.shape and g.shape != (p.numel(),)):
-                _refuse(fn, f"gradient {g.dtype} {tuple(g.shape)} on {g.device} of a parameter {tuple(p.shape)}: "
+                    shape != self.shapes[k] and shape != (self.sizes[k],)):
+                _refuse(fn, f"gradient {g.dtype} {tuple(shape)} on {g.device} of a parameter {tuple(self.shapes[k])}: "
                             "expected dense gradients of one type, in their parameters' shapes or flat, on their "
                             "device")
-        for row, g, p in zip(self.table, grads, self.params):
-            row.grad = None if g is None else g.data_ptr()
-            row.n = 0 if g is None else p.numel()
+            live.append(k)
+        for row, g, n in zip(self.rows, grads, self.sizes):
+            if g is None:
+                row.grad, row.n = None, 0
+            else:
+                row.grad, row.n = g.data_ptr(), n
         self.grad_type = _TYPES[gtype or torch.float32]
         self.grads = grads
+        self.live = live
+        self._count_live()
+
+    def select(self, places):
+        """Let the next steps take these places alone, among those with a gradient, until set_grads."""
+        for k in self.live:
+            self.rows[k].n = 0
+        for k in places:
+            self.rows[k].n = self.sizes[k]
+        self.live = places
+        self._count_live()
+
+    def _count_live(self):
         # what a step writes and autograd may have saved
-        self.updated = [p for part in (self.params, self.master) if part for p, g in zip(part, grads) if g is not None]
+        if len(self.live) == self.n_tensors:
+            self.updated = self.params + (self.master or [])
+        else:
+            self.updated = [part[k] for part in (self.params, self.master) if part for k in self.live]
 
 
     def release_grads(self):
@@ -331,12 +355,13 @@ def dg_adamw_step(p, tensors, stream=None):
 
 
 class AdamW:
-    """AdamW over a list of dense float32 and bf16 tensors, states in 8 or 32 bits, one launch a step and type.
+    """AdamW over a list of dense float32 and bf16 tensors, states in 8 or 32 bits, one launch a step, type and count.
 
     bf16 parameters keep a 32-bit master copy (`master`) or are rounded at random without one; `weight_decay`
     is one value or one for each parameter.  Steps take the parameters' .grad, or the list given to step();
-    a parameter without a gradient is left as it is.  No gradient is held after the step.  The step count lives on the host, so a step is not
-    captured into a graph: graphs take dg_adamw_step with step_dev and lr_dev.
+    a parameter without a gradient is left as it is, and its bias corrections count the steps that had one.  No
+    gradient is held after the step.  The step counts live on the host, so a step is not captured into a graph:
+    graphs take dg_adamw_step with step_dev and lr_dev.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,
@@ -351,6 +376,7 @@ class AdamW:
         else:
             decay = [weight_decay] * len(self.params)
         self.lr, self.betas, self.eps, self.seed, self.steps = lr, betas, eps, int(seed), 0
+        self.counts = [0] * len(self.params)          # the steps that each parameter had a gradient in
         self.groups = []          # one for each parameter type: (places in params, list)
         for dtype in (torch.float32, torch.bfloat16):
             at = [i for i, p in enumerate(self.params) if p.dtype == dtype]
@@ -377,19 +403,27 @@ class AdamW:
         if len(grads) != len(self.params):
             _refuse("AdamW.step", "grads has another length than params")
         for at, tensors in self.groups:
-            for i, row in zip(at, tensors.table):
-                if self.params[i].data_ptr() != (row.param or 0):
+            for i, where in zip(at, tensors.at):
+                if self.params[i].data_ptr() != where:
                     _refuse("AdamW.step", f"parameter {i} lies elsewhere than when the optimizer was made")
         try:
             for at, tensors in self.groups:
                 tensors.set_grads([grads[i] for i in at])
-            for k, (_, tensors) in enumerate(self.groups):
+            for k, (at, tensors) in enumerate(self.groups):
                 plain_bf16 = tensors.param_type == _abi.DG_BF16 and not tensors.table[0].master
-                # a key of its own for each list, whose tensors count from 0
-                p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps,
-                                 step=self.steps + 1, grad_scale=grad_scale,
-                                 seed=(self.seed + (k << 63)) & (1 << 64) - 1, stochastic=int(plain_bf16))
-                dg_adamw_step(p, tensors, stream)
+                of = {}                               # count: the places in the list that it is of
+                for j in tensors.live:
+                    of.setdefault(self.counts[at[j]], []).append(j)
+                for count, now in of.items():
+                    if len(of) > 1:
+                        tensors.select(now)
+                    # a key of its own for each list, whose tensors count from 0
+                    p = adamw_params(lr=self.lr, beta1=self.betas[0], beta2=self.betas[1], eps=self.eps,
+                                     step=count + 1, grad_scale=grad_scale,
+                                     seed=(self.seed + (k << 63)) & (1 << 64) - 1, stochastic=int(plain_bf16))
+                    dg_adamw_step(p, tensors, stream)
+                    for j in now:
+                        self.counts[at[j]] = count + 1
         finally:
             for _, tensors in self.groups:
                 tensors.release_grads()
@@ -414,17 +448,18 @@ class AdamW:
         return [x for _, t in self.groups for part in t.held[1:] for x in part]
 
     def state_dict(self):
-        """The step count and every state tensor (codes and exponents, or values, and masters)."""
-        return {"steps": self.steps, "states": [t.clone() for t in self._states()]}
+        """The step counts and every state tensor (codes and exponents, or values, and masters)."""
+        return {"steps": self.steps, "counts": list(self.counts), "states": [t.clone() for t in self._states()]}
 
     def load_state_dict(self, state):
         mine = self._states()
-        if len(mine) != len(state["states"]) or any(a.shape != b.shape or a.dtype != b.dtype
-                                                    for a, b in zip(mine, state["states"])):
+        counts = state.get("counts", [state["steps"]] * len(self.params))
+        if (len(counts) != len(self.params) or len(mine) != len(state["states"]) or
+                any(a.shape != b.shape or a.dtype != b.dtype for a, b in zip(mine, state["states"]))):
             _refuse("AdamW.load_state_dict", "the states are of other parameters or of another format")
         for a, b in zip(mine, state["states"]):
             a.copy_(b)
-        self.steps = int(state["steps"])
+        self.steps, self.counts = int(state["steps"]), [int(c) for c in counts]
 
 
 # ------------------------------------------------------------------ the head's training loop

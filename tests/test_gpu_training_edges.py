@@ -234,3 +234,32 @@ def test_gradients_outlive_a_step_on_another_stream(dg):
     torch.cuda.synchronize()
     # one step of a gradient of 1: m / (1 - b1) over the root of v / (1 - b2), each within 2^-20
     assert ((p + 1).abs() <= 2.0 ** -19).all() and len(other) == 4
+
+
+def test_a_first_gradient_that_comes_late_counts_from_one(dg):
+    """Bias corrections, random bits and states of each parameter follow its own steps, also through a state_dict."""
+    for bits, dtype in ((32, torch.float32), (8, torch.float32), (8, torch.bfloat16)):
+        g = torch.Generator().manual_seed(bits)
+        base = [torch.randn(n, generator=g).to(dtype) for n in (700, 300, 40)]
+        grads = [[torch.randn(x.shape, generator=g).to(dtype).cuda() for x in base] for _ in range(6)]
+        ps = [x.cuda() for x in base]
+        opt = dg.AdamW(ps, lr=1e-2, betas=(0.9, 0.99), state_bits=bits, seed=9)
+        for t in range(6):
+            if t == 3:
+                state, ps = opt.state_dict(), [x.clone() for x in ps]
+                opt = dg.AdamW(ps, lr=1e-2, betas=(0.9, 0.99), state_bits=bits, seed=9)
+                opt.load_state_dict(state)
+            opt.step([grads[t][0], grads[t][1] if t >= 2 else None, grads[t][2] if t % 2 else None])
+        assert opt.steps == 6
+        # each alone, at its place in the list, stepped only when it has a gradient
+        for i, when in enumerate((range(6), range(2, 6), (1, 3, 5))):
+            x = [b.cuda() for b in base]
+            kind = torch.uint8 if bits == 8 else torch.float32
+            s = [[torch.zeros(b.shape, dtype=kind, device="cuda") for b in base] for _ in range(2)]
+            e = [[torch.zeros(-(-b.numel() // 256), dtype=torch.int8, device="cuda") for b in base] for _ in range(2)]
+            T = dg.AdamWTensors(x, [None] * 3, *s, m_exp=e[0] if bits == 8 else None, v_exp=e[1] if bits == 8 else None)
+            for k, t in enumerate(when):
+                T.set_grads([grads[t][j] if j == i else None for j in range(3)])
+                dg.dg_adamw_step(dg.adamw_params(lr=1e-2, beta1=0.9, beta2=0.99, step=k + 1, seed=9,
+                                                 stochastic=int(dtype == torch.bfloat16)), T)
+            assert torch.equal(x[i], ps[i])
