@@ -469,18 +469,23 @@ class HeadTrainer:
     accumulate(h, targets) adds the gradients of one batch and returns (loss, dh): the weighted mean loss as
     a device scalar and the hidden states' gradient, for a denoiser to go on with; update() applies AdamW;
     step() does both.  They count batches and steps on the host and are not captured into graphs (capture
-    dg_xent_forward, dg_xent_backward and dg_adamw_step).  serving() gives the head in the layout that dg_denoise_step reads.
+    dg_xent_forward, dg_xent_backward and dg_adamw_step).  serving() gives the head in the layout that
+    dg_denoise_step reads.
+
+    The head's gradient dW is held in bf16 while a step is one batch, and in float32 from the first step that
+    accumulates more: a bf16 sum drops what is below half a step of it.  grad_dtype fixes the type.
     """
 
     def __init__(self, W, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=8, master=False,
-                 grad_dtype=torch.bfloat16, temperature=1.0, ignore_index=-100, seed=0):
+                 grad_dtype=None, temperature=1.0, ignore_index=-100, seed=0):
         if W.dim() != 2 or W.dtype != torch.bfloat16 or not W.is_contiguous():
             _refuse("HeadTrainer", f"W is {W.dtype} {tuple(W.shape)}, expected a dense torch.bfloat16 [V, d]")
-        if grad_dtype not in _TYPES:
+        if grad_dtype is not None and grad_dtype not in _TYPES:
             _refuse("HeadTrainer", f"grad_dtype is {grad_dtype}, expected bfloat16 or float32")
         self.W = W.detach()
         self.optimizer = AdamW([self.W], lr, betas, eps, weight_decay, state_bits, master, seed)
-        self.dW = torch.empty(W.shape, dtype=grad_dtype, device=W.device)
+        self.dW = torch.empty(W.shape, dtype=grad_dtype or torch.bfloat16, device=W.device)
+        self.widens = grad_dtype is None
         self.temperature, self.ignore_index = temperature, ignore_index
         self.batches = 0          # batches whose gradients dW holds
         self._ws = None           # the workspace of the largest batch so far
@@ -500,6 +505,8 @@ class HeadTrainer:
         w = kept.float() if weight is None else torch.where(kept, weight, 0.0).float()
         dloss = torch.where(w != 0, w / w.sum(), 0)         # 0 also where nothing counts
         dh = torch.empty((p.n, p.hidden), dtype=torch.bfloat16, device=self.W.device)
+        if self.batches > 0 and self.widens and self.dW.dtype != torch.float32:
+            self.dW = self.dW.float()
         dg_xent_backward(p, h, self.W, targets, loss, lse, dloss, dh, self.dW, self._ws)
         self.batches += 1
         return torch.where(dloss != 0, dloss * loss, 0).sum(), dh

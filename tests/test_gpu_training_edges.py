@@ -263,3 +263,25 @@ def test_a_first_gradient_that_comes_late_counts_from_one(dg):
                 dg.dg_adamw_step(dg.adamw_params(lr=1e-2, beta1=0.9, beta2=0.99, step=k + 1, seed=9,
                                                  stochastic=int(dtype == torch.bfloat16)), T)
             assert torch.equal(x[i], ps[i])
+
+
+def test_many_batches_are_accumulated_without_losing_any(dg):
+    """64 batches at the default type: the sum of their gradients, where a bf16 sum would drop what is below half a
+    step of it."""
+    V, d, n, k = 300, 64, 40, 64
+    h, W, y, w = inputs(n, V, d, seed=3)
+    tr = dg.HeadTrainer(W.cuda())
+    one = dg.HeadTrainer(W.cuda().clone(), grad_dtype=torch.float32)
+    hd, yd, wd = h.cuda(), y.cuda(), w.cuda()
+    one.accumulate(hd, yd, wd)
+    for _ in range(2):                        # the first steps to accumulate, and the ones after it
+        for _ in range(k):
+            tr.accumulate(hd, yd, wd)
+        want = k * one.dW.double()
+        # each of the k - 1 fp32 sums is off by 2^-24 of itself, the first batch by bf16's half step
+        assert ((tr.dW.double() - want).abs() <= (k * 2.0 ** -24 + 2.0 ** -8 / k) * want.abs() + 1e-38).all()
+        tr.batches = 0
+    tr.batches = k
+    before = tr.W.clone()
+    tr.update()
+    assert tr.optimizer.steps == 1 and not torch.equal(tr.W, before)
