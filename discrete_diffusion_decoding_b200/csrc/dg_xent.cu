@@ -1456,6 +1456,9 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     const size_t dw_bytes = static_cast<size_t>(p->vocab) * p->hidden * (p->dw_type == DG_FP32 ? 4 : 2);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!aligned(dW_dev, 16) || !aligned(dh_dev, 16)) return DG_EINVAL;
+    // the products read W after the first of its gradient's rows are written, and no positions still zero dW
+    const size_t w_bytes = static_cast<size_t>(p->vocab) * p->hidden * 2;
+    if (dW_dev && W_dev && overlap(dW_dev, dw_bytes, W_dev, w_bytes)) return DG_EINVAL;
     if (p->n == 0) {
         if (dW_dev && !p->dw_accumulate && cudaMemsetAsync(dW_dev, 0, dw_bytes, s) != cudaSuccess) return DG_ECUDA;
         return DG_OK;
@@ -1464,10 +1467,7 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
     if (!aligned(h_dev, 2) || !aligned(W_dev, 16) || !aligned(targets_dev, p->target_type == DG_INT64 ? 8 : 4) ||
         !aligned(loss_dev, 4) || !aligned(lse_dev, 4) || !aligned(dloss_dev, 4) || !aligned(workspace_dev, 256))
         return DG_EINVAL;
-    const size_t w_bytes = static_cast<size_t>(p->vocab) * p->hidden * 2;
     const size_t dh_bytes = static_cast<size_t>(p->n) * p->hidden * 2;
-    // the products read W after the first of its gradient's rows are written
-    if (dW_dev && overlap(dW_dev, dw_bytes, W_dev, w_bytes)) return DG_EINVAL;
     const size_t h_bytes = 2 * (static_cast<size_t>(p->n - 1) * (p->h_stride ? p->h_stride : p->hidden) + p->hidden);
     if (dh_dev && (overlap(dh_dev, dh_bytes, W_dev, w_bytes) || overlap(dh_dev, dh_bytes, h_dev, h_bytes)))
         return DG_EINVAL;

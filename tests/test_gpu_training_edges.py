@@ -285,3 +285,16 @@ def test_many_batches_are_accumulated_without_losing_any(dg):
     before = tr.W.clone()
     tr.update()
     assert tr.optimizer.steps == 1 and not torch.equal(tr.W, before)
+
+
+# ------------------------------------------------------------------ overlaps, captures, streams
+def test_no_positions_do_not_clear_the_head(dg):
+    """dW on top of W is refused whatever the number of positions."""
+    W = torch.randn(300, 64).bfloat16().cuda()
+    before = W.clone()
+    h = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    y, f = torch.empty(0, dtype=torch.int32, device="cuda"), torch.empty(0, device="cuda")
+    p = dg.xent_params(0, 300, 64)
+    with pytest.raises(dg.DgError):
+        dg.dg_xent_backward(p, h, W, y, f, f, f, None, W, dg.XentWorkspace(p))
+    assert torch.equal(W, before)
