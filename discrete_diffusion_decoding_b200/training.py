@@ -41,8 +41,11 @@ def _tensor(fn, name, t, dtypes, shape, device):
                     f"expected dense {' or '.join(str(d) for d in dtypes)} {tuple(shape)} on {device}")
 
 
-def _refuse_capture(fn, instead):
+def _refuse_capture(fn, instead, stream=None):
     """Calls that count on the host: a graph would repeat the counts of its capture."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _refuse_capture(fn, instead)
     if torch.cuda.is_available() and torch.cuda.is_current_stream_capturing():
         _refuse(fn, f"the stream is being captured; capture {instead}")
 
@@ -398,7 +401,7 @@ class AdamW:
             _refuse("AdamW", "parameters must be float32 or bfloat16")
 
     def step(self, grads=None, grad_scale=1.0, stream=None):
-        _refuse_capture("AdamW.step", "dg_adamw_step with step_dev")
+        _refuse_capture("AdamW.step", "dg_adamw_step with step_dev", stream)
         grads = [p.grad for p in self.params] if grads is None else list(grads)
         if len(grads) != len(self.params):
             _refuse("AdamW.step", "grads has another length than params")

@@ -298,3 +298,17 @@ def test_no_positions_do_not_clear_the_head(dg):
     with pytest.raises(dg.DgError):
         dg.dg_xent_backward(p, h, W, y, f, f, f, None, W, dg.XentWorkspace(p))
     assert torch.equal(W, before)
+
+
+def test_a_step_on_a_stream_under_capture_is_refused(dg):
+    """Also where that stream is not the current one."""
+    W = torch.ones(64, 8, dtype=torch.bfloat16, device="cuda")
+    opt, x, g = dg.AdamW([W]), torch.zeros(4, device="cuda"), torch.cuda.CUDAGraph()
+    grad, side, other = torch.ones_like(W), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        x.add_(1)
+        with torch.cuda.stream(other):
+            with pytest.raises(dg.DgError, match="captured"):
+                opt.step([grad], stream=side)
+    assert opt.steps == 0
