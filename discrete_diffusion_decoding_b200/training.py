@@ -7,6 +7,7 @@ current stream.
 """
 
 import ctypes
+import math
 
 import torch
 
@@ -50,6 +51,13 @@ def _refuse_capture(fn, instead, stream=None):
         _refuse(fn, f"the stream is being captured; capture {instead}")
 
 
+def _check_place(fn, device, stream):
+    if device.index is None:      # host and meta tensors have none
+        _refuse(fn, f"tensors are on {device}, expected a CUDA device")
+    if stream is not None and stream.device != device:
+        _refuse(fn, f"the stream is on {stream.device}, the tensors on {device}")
+
+
 def _call(fn, device, stream, written, *args):
     """The library's entry point `fn` on `stream`, or the device's current stream, with the device made current.
 
@@ -57,14 +65,8 @@ def _call(fn, device, stream, written, *args):
     of them refuses (a replay of a captured call is not counted).
     """
     index = device.index
-    if index is None:             # host and meta tensors have none
-        _refuse(fn, f"tensors are on {device}, expected a CUDA device")
-    if stream is None:
-        handle = _current_stream(index)
-    elif stream.device != device:
-        _refuse(fn, f"the stream is on {stream.device}, the tensors on {device}")
-    else:
-        handle = stream.cuda_stream
+    _check_place(fn, device, stream)
+    handle = _current_stream(index) if stream is None else stream.cuda_stream
     if _current_device() == index:
         check(fn, getattr(lib(), fn)(*args, handle))
     else:
@@ -274,6 +276,8 @@ class AdamWTensors:
             n = self.sizes[i]
             row = self.rows[i]
             row.param, row.n, row.weight_decay = _ptr(p), n, decay[i]
+            if not math.isfinite(row.weight_decay):          # as float32
+                _refuse(fn, f"weight_decay {decay[i]} is not finite")
             spans.append((p.data_ptr(), n * p.element_size()))
             for name, x in lists.items():
                 t = x[i]
@@ -409,6 +413,9 @@ class AdamW:
             for i, where in zip(at, tensors.at):
                 if self.params[i].data_ptr() != where:
                     _refuse("AdamW.step", f"parameter {i} lies elsewhere than when the optimizer was made")
+        # a step is whole or not at all: what one list would refuse is refused before another one's launch
+        for _, tensors in self.groups:
+            _check_place("AdamW.step", tensors.device, stream)
         try:
             for at, tensors in self.groups:
                 tensors.set_grads([grads[i] for i in at])

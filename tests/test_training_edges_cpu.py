@@ -60,3 +60,38 @@ def test_gradients_and_states_have_their_parameters_shape(dg):
     with pytest.raises(dg.DgError):
         dg.AdamWTensors([z(4, 6)], [z(4, 6)], [z(6, 4)], [z(4, 6)])
     assert dg.AdamWTensors([z(4, 6)], [z(24)], [z(24)], [z(24)]).table[0].n == 24
+
+
+def test_a_step_is_whole_or_not_at_all(dg, monkeypatch):
+    """What one list's launch would refuse is refused before another list's launch."""
+    from types import SimpleNamespace
+    from discrete_diffusion_decoding_b200 import training
+    launched = []
+    real = training.lib()
+    fake = SimpleNamespace(dg_adamw_step=lambda *a: launched.append(a) or 0,
+                           dg_adamw_params_default=real.dg_adamw_params_default)
+    monkeypatch.setattr(training, "lib", lambda: fake)
+    monkeypatch.setattr(training, "_current_stream", lambda i: 0)
+    monkeypatch.setattr(training, "_current_device", lambda: 0)
+    monkeypatch.setattr(training, "_refuse_capture", lambda *a: None)
+    ps = [torch.zeros(5), torch.zeros(5, dtype=torch.bfloat16)]
+
+    def step(devices, stream=None):
+        opt = dg.AdamW(ps)
+        for (_, tensors), d in zip(opt.groups, devices):
+            monkeypatch.setattr(tensors, "set_grads", lambda g, t=tensors: (
+                setattr(t, "grads", g), setattr(t, "live", [0]), setattr(t, "updated", [])))
+            tensors.device = torch.device(d)
+        opt.step([torch.ones_like(p) for p in ps], stream=stream)
+        return opt
+
+    assert step(["cuda:0", "cuda:0"]).steps == 1 and len(launched) == 2
+    launched.clear()
+    with pytest.raises(dg.DgError):
+        step(["cuda:0", "cpu"])
+    with pytest.raises(dg.DgError):
+        step(["cuda:0", "cuda:1"], SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=0))
+    assert not launched
+    for decay in (float("nan"), float("inf"), 1e39, [0.0, -float("inf")]):
+        with pytest.raises(dg.DgError):
+            dg.AdamW(ps, weight_decay=decay)
