@@ -506,8 +506,14 @@ class HeadTrainer:
         _refuse_capture("HeadTrainer.accumulate", "dg_xent_forward and dg_xent_backward")
         p = xent_params(targets.numel(), self.W.shape[0], self.W.shape[1], temperature=self.temperature,
                         ignore_index=self.ignore_index, dw_accumulate=int(self.batches > 0))
-        if self._ws is None or self._ws.nbytes < xent_workspace_size(p):
+        with torch.cuda.device(self.W.device):
+            size = xent_workspace_size(p)
+        if self._ws is None or self._ws.nbytes < size:
             self._ws = XentWorkspace(p, self.W.device)
+        # a larger batch renews it, and a second one dW, perhaps while another stream than their own works in them
+        here = torch.cuda.current_stream(self.W.device)
+        self._ws.buf.record_stream(here)
+        self.dW.record_stream(here)
         loss = torch.empty(p.n, dtype=torch.float32, device=self.W.device)
         lse = torch.empty_like(loss)
         dg_xent_forward(p, h, self.W, targets, loss, lse, self._ws)

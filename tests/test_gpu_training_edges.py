@@ -312,3 +312,23 @@ def test_a_step_on_a_stream_under_capture_is_refused(dg):
             with pytest.raises(dg.DgError, match="captured"):
                 opt.step([grad], stream=side)
     assert opt.steps == 0
+
+
+def test_a_trainer_moved_between_streams_keeps_its_workspace(dg):
+    """A larger batch on another stream renews the workspace: the old one is not handed out while it is in use."""
+    V, d = 20000, 512
+    h, W, y, w = inputs(300, V, d, seed=5)
+    hd, yd = h.cuda(), y.cuda()
+    want = dg.HeadTrainer(W.cuda()).accumulate(hd[:20], yd[:20])[1]
+    tr = dg.HeadTrainer(W.cuda())
+    tr.accumulate(hd[:20], yd[:20])
+    size, main, side = tr._ws.nbytes, torch.cuda.current_stream(), torch.cuda.Stream()
+    side.wait_stream(main)
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        tr.batches = 0
+        got = tr.accumulate(hd[:20], yd[:20])[1]
+        tr.accumulate(hd, yd)
+    junk = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and (junk == 0).all()
