@@ -163,7 +163,8 @@ def tile_head(W, stream=None):
 
 
 def dg_debug_set_counter_wait_limit(ns):
-    """Testing hook: limit the fused kernel's waits on other CTAs' counters to ns (0: the 2 s default)."""
+    """Testing hook: limit the fused kernel's waits on other CTAs' counters, and the waits inside the training
+    products, to ns (0: the 2 s default)."""
     check("dg_debug_set_counter_wait_limit", lib().dg_debug_set_counter_wait_limit(int(ns)))
 
 

@@ -235,6 +235,8 @@ dg_status plan_current_device(const dg_params* p, Plan* pl) {
 
 void set_last_launches(int n) { g_last_launches = n; }
 
+unsigned long long counter_wait_ns() { return g_counter_wait_ns; }
+
 PartialLayout partial_layout(int N, int d) {
     PartialLayout P{};
     size_t o = 0;

@@ -46,6 +46,9 @@ dg_status make_plan(const dg_params* p, int pairs, Plan* pl);
 // Resolve the plan of p on the current device (resident_pairs + make_plan).
 dg_status plan_current_device(const dg_params* p, Plan* pl);
 
+// The limit that dg_debug_set_counter_wait_limit set on this thread (DG_WAIT_LIMIT_NS unless one did).
+unsigned long long counter_wait_ns();
+
 // Records how many kernels the calling entry point launched (dg_last_launch_count).
 void set_last_launches(int n);
 

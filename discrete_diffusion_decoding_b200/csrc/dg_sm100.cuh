@@ -154,18 +154,19 @@ __device__ __forceinline__ void raise_pair_abort(volatile int* abort) {
 
 // Bounded wait for the phase with the given parity to complete.  On timeout, or
 // when another role has already raised `abort`, records `code` in *err (first
-// error wins), raises the pair's abort flags and returns false.
+// error wins), raises the pair's abort flags and returns false.  A shorter limit
+// (a test's) is looked at after every try.
 template <bool kClusterAcquire = false>
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          int* err, int code) {
+                                          int* err, int code, uint64_t limit_ns = DG_WAIT_LIMIT_NS) {
     const uint32_t a = smem_u32(bar);
     if (kClusterAcquire ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
     const uint64_t t0 = global_ns();
     while (true) {
-        for (int i = 0; i < 32; ++i)
+        for (int i = 0; i < (limit_ns < DG_WAIT_LIMIT_NS ? 1 : 32); ++i)
             if (kClusterAcquire ? mbar_try_wait_cluster(a, parity) : mbar_try_wait(a, parity)) return true;
         if (*abort) return false;
-        if (global_ns() - t0 > DG_WAIT_LIMIT_NS) {
+        if (global_ns() - t0 > limit_ns) {
             atomicCAS(err, 0, code);
             raise_pair_abort(abort);
             return false;

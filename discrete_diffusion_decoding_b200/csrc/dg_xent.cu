@@ -250,6 +250,7 @@ struct GemmArgs {
     CUtensorMap g_mn, h_mn;          // G and packed h, MN-major: dW
     CUtensorMap g_out, dw_out;       // G and a bf16 dW as outputs, boxes of 64 columns x 32 rows
     Packed pk;
+    unsigned long long wait_ns;      // limit of each wait but those of the drains
     uint32_t* ticket;                // this launch's counter
     int vocab, d, d_tiles;
     float scale_log2;                // log2(e) / T
@@ -618,7 +619,8 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
     auto fetch = [&](uint32_t n, Item& it) {
         if (n == 0) return m_tiles_or_dw > 0 && item_at<kForward>(a, pair, m_tiles, rows, it);
         const uint32_t s = (n - 1) % kSched;
-        if (!mbar_wait<true>(&sched_full[s], ((n - 1) / kSched) & 1, &abort_flag, err, kErrSched)) return false;
+        if (!mbar_wait<true>(&sched_full[s], ((n - 1) / kSched) & 1, &abort_flag, err, kErrSched, a.wait_ns))
+            return false;
         const volatile uint32_t* w = sched_item[s];
         it = Item{static_cast<int>(w[0]), static_cast<int>(w[1]), static_cast<int>(w[2]), static_cast<int>(w[3]),
                   static_cast<int>(w[4]), static_cast<int>(w[5]), static_cast<int>(w[6])};
@@ -658,7 +660,8 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
                 for (int k = 0; k < it.kbs; ++k, ka += kK, kb += kK) {
                     const int need = 1 + it.tiles;
                     while (taken + need > kBoxes || issued - freed >= kMaxStages) {
-                        if (!mbar_wait(&empty[freed % kMaxStages], (freed / kMaxStages) & 1, &abort_flag, err, kErrEmpty)) {
+                        if (!mbar_wait(&empty[freed % kMaxStages], (freed / kMaxStages) & 1, &abort_flag, err,
+                                       kErrEmpty, a.wait_ns)) {
                             ok = false;
                             break;
                         }
@@ -758,14 +761,15 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
                     }
                 };
                 auto landed = [&](uint32_t stage) {
-                    if (!mbar_wait(&full[stage % kMaxStages], (stage / kMaxStages) & 1, &abort_flag, err, kErrFull))
+                    if (!mbar_wait(&full[stage % kMaxStages], (stage / kMaxStages) & 1, &abort_flag, err, kErrFull,
+                                   a.wait_ns))
                         return false;
                     tc_fence_after();
                     return true;
                 };
                 auto acc_ready = [&](int acc) {
                     if (uses[acc] > 0 &&
-                        !mbar_wait(&acc_free[acc], (uses[acc] - 1) & 1, &abort_flag, err, kErrAccFree))
+                        !mbar_wait(&acc_free[acc], (uses[acc] - 1) & 1, &abort_flag, err, kErrAccFree, a.wait_ns))
                         return false;
                     ++uses[acc];
                     tc_fence_after();
@@ -813,7 +817,7 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
             for (uint32_t k = 0; more; ++k) {       // item k + 1
                 const uint32_t s = k % kSched;
                 if (k >= kSched &&
-                    !mbar_wait<true>(&sched_free[s], ((k / kSched) - 1) & 1, &abort_flag, err, kErrSchedFree))
+                    !mbar_wait<true>(&sched_free[s], ((k / kSched) - 1) & 1, &abort_flag, err, kErrSchedFree, a.wait_ns))
                     break;
                 more = item_at<kForward>(a, pairs + static_cast<int>(atomicAdd(a.ticket, 1u)), m_tiles, rows, it);
                 if (!more) it = Item{-1, 0, 0, 0, 0, 0, 0};
@@ -842,7 +846,8 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
             if (first) release(n);
             for (int j = 0; j < it.tiles; ++j) {
                 const int buf = next ^ j;
-                if (group_any(group, !mbar_wait(&acc_full[buf], uses[buf] & 1, &abort_flag, err, kErrAccFull))) {
+                if (group_any(group, !mbar_wait(&acc_full[buf], uses[buf] & 1, &abort_flag, err, kErrAccFull,
+                                                a.wait_ns))) {
                     ok = false;
                     break;
                 }
@@ -890,6 +895,7 @@ constexpr int kFewThreads = 256;
 struct FewArgs {
     CUtensorMap h, w;        // boxes of 64 columns x columns / 128 rows, K-major
     Packed pk;
+    unsigned long long wait_ns;
     int vocab, d, columns;   // columns of a tile: 16 or 32
     float scale_log2;
     float2* part;            // [position][4 gridDim.x]
@@ -908,7 +914,8 @@ __device__ __forceinline__ void few_epilogue(const FewArgs& a, uint32_t tmem, ui
     int n = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++n) {
         const int buf = n & 1;
-        if (group_any(0, !mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, a.pk.err, kErrAccFull))) return;
+        if (group_any(0, !mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, a.pk.err, kErrAccFull, a.wait_ns)))
+            return;
         tc_fence_after();
         uint32_t r[kColumns];
 #pragma unroll
@@ -997,7 +1004,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
                 for (int k = 0; k < kbs; ++k) {
                     const uint32_t s = issued % stages;
                     if (issued >= static_cast<uint32_t>(stages) &&
-                        !mbar_wait(&empty[s], ((issued / stages) - 1) & 1, &abort_flag, err, kErrEmpty)) {
+                        !mbar_wait(&empty[s], ((issued / stages) - 1) & 1, &abort_flag, err, kErrEmpty, a.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -1027,11 +1034,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
             bool ok = true;
             for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x, ++n) {
                 const int buf = n & 1;
-                if (n >= 2 && !mbar_wait(&acc_free[buf], ((n >> 1) - 1) & 1, &abort_flag, err, kErrAccFree)) break;
+                if (n >= 2 &&
+                    !mbar_wait(&acc_free[buf], ((n >> 1) - 1) & 1, &abort_flag, err, kErrAccFree, a.wait_ns))
+                    break;
                 tc_fence_after();
                 for (int k = 0; k < kbs; ++k, ++used) {
                     const uint32_t s = used % stages;
-                    if (!mbar_wait(&full[s], (used / stages) & 1, &abort_flag, err, kErrFull)) {
+                    if (!mbar_wait(&full[s], (used / stages) & 1, &abort_flag, err, kErrFull, a.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -1349,6 +1358,7 @@ GemmArgs gemm_args(const dg_xent_params* p, const XentPlan& q, void* ws) {
     GemmArgs a;
     std::memset(&a, 0, sizeof(a));
     a.pk = packed_of(q, ws);
+    a.wait_ns = host::counter_wait_ns();
     a.vocab = p->vocab;
     a.d = p->hidden;
     a.d_tiles = q.d_tiles;
@@ -1414,6 +1424,7 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
     if (few) {
         std::memset(&fa, 0, sizeof(fa));
         fa.pk = pk;
+        fa.wait_ns = host::counter_wait_ns();
         fa.vocab = p->vocab;
         fa.d = p->hidden;
         fa.columns = p->n <= 16 ? 16 : kFewRows;

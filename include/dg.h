@@ -224,7 +224,8 @@ dg_status dg_debug_set_error(const dg_params* p, void* workspace_dev, size_t wor
  * Testing hook for the timeout path (not on the pages): the fused kernel launched by later
  * calls on this host thread limits each of its waits on other CTAs' progress counters (the
  * row-maximum exchange and the probability tiles of the group) to `ns` nanoseconds instead
- * of 2 s; 0 restores 2 s.  A wait that runs out makes the kernel leave early and record
+ * of 2 s; 0 restores 2 s.  So does every wait between the roles of the training products
+ * (dg_xent_forward, dg_xent_backward: NaN results).  A wait that runs out makes the kernel leave early and record
  * the error word exactly as a stalled peer would (DG_ETIMEOUT from dg_stop_check, poisoned
  * results).  The waits that drain a CTA's own loads and tensor-core operations keep their
  * 2 s limit (they wait for the CTA's own loads to land), so none is in flight when a CTA

@@ -2,6 +2,7 @@
 the gradients' largest entries, logits that are not finite, values below the normal range, steps and streams."""
 
 import gc
+import time
 import weakref
 
 import numpy as np
@@ -10,7 +11,7 @@ import torch
 
 from oracle import adamw, xent
 from test_gpu_adamw import check_roots
-from test_gpu_xent import IGNORE, inputs, run
+from test_gpu_xent import IGNORE, check, inputs, run
 
 pytestmark = pytest.mark.gpu
 
@@ -332,3 +333,38 @@ def test_a_trainer_moved_between_streams_keeps_its_workspace(dg):
     junk = torch.zeros(size, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(got, want) and (junk == 0).all()
+
+# ------------------------------------------------------------------ waits that run out, and the largest hidden size
+@pytest.mark.parametrize("n", [3, 40])
+def test_waits_that_run_out(dg, n):
+    """With a limit that the long sums of the largest hidden size exceed, the kernels leave on their own and at once:
+    NaN in loss, lse and both gradients, 0 at ignored positions.  The next calls with the same workspace are right."""
+    V, d = 700, 65536
+    g = torch.Generator().manual_seed(n)
+    W = (torch.randn(V, d, generator=g) / 64).bfloat16()
+    h = (torch.randn(n, d, generator=g) / 4).bfloat16()
+    y, dl = torch.randint(0, V, (n,), generator=g).int(), torch.rand(n, generator=g) + 0.5
+    y[1] = IGNORE
+    p = dg.xent_params(n, V, d)
+    ws = dg.XentWorkspace(p)
+    want = run(dg, h, W, y, dl, ws=ws)
+    check(h, W, y, dl, 1.0, want)
+    hd, Wd, yd, dld = h.cuda(), W.cuda(), y.cuda(), dl.cuda()
+    loss, lse = (torch.from_numpy(x).float().cuda() for x in want[:2])
+    bad, bad_lse, dh, dW = (torch.zeros_like(x) for x in (loss, lse, hd, Wd))
+    torch.cuda.synchronize()
+    start = time.time()
+    try:
+        dg.dg_debug_set_counter_wait_limit(1)          # 1 ns: a wait not satisfied at once runs out
+        dg.dg_xent_forward(p, hd, Wd, yd, bad, bad_lse, ws)
+        dg.dg_xent_backward(p, hd, Wd, yd, loss, lse, dld, dh, dW, ws)
+        torch.cuda.synchronize()
+    finally:
+        dg.dg_debug_set_counter_wait_limit(0)
+    # well under the 2 s limit of a drain: every drain ended on the loads and products in flight
+    assert time.time() - start < 1.0
+    kept = yd != IGNORE
+    assert torch.isnan(bad[kept]).all() and torch.isnan(bad_lse[kept]).all() and bad[1] == 0 and bad_lse[1] == 0
+    assert torch.isnan(dh[kept]).all() and torch.isnan(dW).all() and (dh[1] == 0).all()
+    for a, b in zip(run(dg, h, W, y, dl, ws=ws), want):
+        assert np.array_equal(a, b)
