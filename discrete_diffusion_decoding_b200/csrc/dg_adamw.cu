@@ -489,6 +489,9 @@ struct Lane {
     }
 };
 
+// Four CTAs an SM leave 64 registers, and three of the four kernels for bf16 parameters with 8-bit states then keep up
+// to 6 words in local memory.  With three CTAs and 80 registers none does, and they are slower: 100 million
+// parameters with bf16 gradients 266 -> 289 us, with fp32 ones 268 -> 289, with a master 281 -> 301 and 298 -> 309.
 template <class P, class G, bool kState8, bool kMaster, int kCap>
 __global__ void __launch_bounds__(kWarps * 32, 4) dg_adamw_kernel(const __grid_constant__ Args<kCap> a) {
     // the tensor this CTA works on

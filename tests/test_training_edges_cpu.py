@@ -1,9 +1,15 @@
 """Refusals of the training entry points at the edges of what they document, without a GPU."""
 
 import ctypes
+import os
+import re
+import shutil
+import subprocess
 
 import pytest
 import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -95,3 +101,23 @@ def test_a_step_is_whole_or_not_at_all(dg, monkeypatch):
     for decay in (float("nan"), float("inf"), 1e39, [0.0, -float("inf")]):
         with pytest.raises(dg.DgError):
             dg.AdamW(ps, weight_decay=decay)
+
+
+def test_the_update_keeps_to_registers_but_for_a_few_words(tmp_path):
+    """ptxas reports spills of the AdamW kernels only for bf16 parameters with 8-bit states, and at most 24 bytes."""
+    nvcc = next((c for c in (os.environ.get("NVCC"), "/usr/local/cuda/bin/nvcc", shutil.which("nvcc"))
+                 if c and os.path.exists(c)), None)
+    if nvcc is None:
+        pytest.skip("nvcc not available")
+    src = os.path.join(ROOT, "discrete_diffusion_decoding_b200", "csrc", "dg_adamw.cu")
+    out = subprocess.run([nvcc, "-gencode", "arch=compute_100a,code=sm_100a", "-O3", "-std=c++17", "-Xptxas", "-v", "-c",
+                          "-o", str(tmp_path / "k.o"), src], capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0, out.stderr[-2000:]
+    found = re.findall(r"Compiling entry function '(\S+)'.*?(\d+) bytes spill stores, (\d+) bytes spill loads",
+                       out.stderr, re.S)
+    assert len(found) == 24
+    for name, *spills in found:
+        # <parameter, gradient, 8-bit states, ...> as the name holds them: the parameter's type, then the first flag
+        of_bf16 = "kernelI13__nv_bfloat16" in name
+        state8 = name.split("Lb")[1][0] == "1"
+        assert max(map(int, spills)) <= (24 if of_bf16 and state8 else 0), name
