@@ -368,3 +368,106 @@ def test_waits_that_run_out(dg, n):
     assert torch.isnan(dh[kept]).all() and torch.isnan(dW).all() and (dh[1] == 0).all()
     for a, b in zip(run(dg, h, W, y, dl, ws=ws), want):
         assert np.array_equal(a, b)
+
+
+# ------------------------------------------------------------------ the limits that the header states
+@pytest.mark.parametrize("n,V,d,scratch", [
+    (63, 5000, 64, 0), (64, 5000, 64, 0), (65, 5000, 64, 0),       # around one stage of positions
+    (255, 3000, 72, 0), (256, 2999, 72, 0), (257, 3001, 72, 0),    # around one tile
+    (40, 768, 16, 0), (40, 769, 16, 0), (40, 40000, 16, 0),        # dh in one part, in two, in 70
+    (256, 147 * 256, 8, 0), (256, 148 * 256, 8, 0), (256, 149 * 256 + 1, 8, 0),   # one tile an item, two
+    (300, 74 * 256, 264, 0), (300, 75 * 256, 520, 0),
+    (300, 5000, 264, 2 * 2 * 512 * 256), (300, 5000, 264, 2 * 2 * 512 * 256 * 10 - 1),    # pieces of one tile, of nine
+])
+def test_around_the_limits_of_tiles_items_and_pieces(dg, n, V, d, scratch):
+    h, W, y, dl = inputs(n, V, d, seed=n + V)
+    check(h, W, y, dl, 1.0, run(dg, h, W, y, dl, scratch_bytes=scratch))
+
+
+def test_the_most_positions(dg):
+    """2^22 positions, against float64 on the device, some thousands at a time."""
+    n, V, d = 1 << 22, 300, 8
+    g = torch.Generator(device="cuda").manual_seed(0)
+    W = (torch.randn(V, d, device="cuda", generator=g) * 0.5).bfloat16()
+    h = torch.randn(n, d, device="cuda", generator=g).bfloat16()
+    y = torch.randint(0, V, (n,), device="cuda", generator=g).int()
+    y[torch.rand(n, device="cuda", generator=g) < 0.2] = IGNORE
+    dl = torch.rand(n, device="cuda", generator=g) + 0.5
+    p = dg.xent_params(n, V, d)
+    ws = dg.XentWorkspace(p)
+    loss, lse = torch.full((n,), 7.0, device="cuda"), torch.full((n,), 7.0, device="cuda")
+    dg.dg_xent_forward(p, h, W, y, loss, lse, ws)
+    dh, dW = torch.full_like(h, 7.0), torch.full((V, d), 7.0, device="cuda")
+    dg.dg_xent_backward(p, h, W, y, loss, lse, dl, dh, dW, ws)
+    W64 = W.double()
+    sums, sizes = torch.zeros_like(W64), torch.zeros_like(W64)
+    # 8 products and fp32 factors: every logit is within 2^-19 of its magnitude (8 x 0.5 x 4 x 4 at most 64) and lse
+    # near 6 within 2^-21 of it
+    dz = 2.0 ** -13
+    step = 1 << 18
+    for a in range(0, n, step):
+        at = slice(a, a + step)
+        kept = y[at] != IGNORE
+        yy = torch.where(kept, y[at], 0).long()
+        h64 = torch.where(kept[:, None], h[at].double(), 0)
+        z = h64 @ W64.T
+        want_lse = torch.logsumexp(z, 1)
+        want = want_lse - z.gather(1, yy[:, None])[:, 0]
+        assert ((loss[at] - torch.where(kept, want, 0)).abs() <= 2 * dz * kept).all()
+        assert ((lse[at] - torch.where(kept, want_lse, 0)).abs() <= 2 * dz * kept).all()
+        G = torch.exp(z - want_lse[:, None])
+        G[torch.arange(len(yy), device="cuda"), yy] -= 1
+        G *= torch.where(kept, dl[at].double(), 0)[:, None]
+        off, tol = (dh[at] - G @ W64).abs(), (2.0 ** -8 + 3 * dz) * (G.abs() @ W64.abs())
+        assert (off <= tol + 2.0 ** -8 * (G @ W64).abs() + 1e-38).all()
+        sums += G.T @ h64
+        sizes += G.abs().T @ h64.abs()
+    assert ((dW - sums).abs() <= (2.0 ** -8 + 3 * dz + (n / 16) * 2.0 ** -23) * sizes).all()
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_the_largest_vocabulary(dg, n):
+    """2^28 rows, against float64 on the device, a part of the vocabulary at a time; targets at both ends."""
+    V, d = 1 << 28, 8
+    g = torch.Generator(device="cuda").manual_seed(n)
+    W = torch.empty(V, d, dtype=torch.bfloat16, device="cuda").normal_(0.0, 0.25, generator=g)
+    y = torch.randint(0, V, (n,), device="cuda", generator=g).int()
+    y[0], y[1], y[2] = V - 1, 0, (1 << 27) + 1
+    # half of the probability at the target of two positions, far less at the others
+    h = torch.randn(n, d, device="cuda", generator=g)
+    h[:2] = W[y[:2].long()].float() * (20 / (W[y[:2].long()].float() ** 2).sum(1, keepdim=True))
+    h, dl = h.bfloat16(), torch.rand(n, device="cuda", generator=g) + 0.5
+    p = dg.xent_params(n, V, d)
+    ws = dg.XentWorkspace(p)
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dg.dg_xent_forward(p, h, W, y, loss, lse, ws)
+    dh, dW = torch.empty_like(h), torch.empty_like(W)
+    dg.dg_xent_backward(p, h, W, y, loss, lse, dl, dh, dW, ws)
+    h64, step = h.double(), 1 << 22
+    total = torch.full((n,), -float("inf"), dtype=torch.float64, device="cuda")
+    most = 0.0
+    for a in range(0, V, step):
+        W64 = W[a:a + step].double()
+        total = torch.logaddexp(total, torch.logsumexp(h64 @ W64.T, 1))
+        most = max(most, float((h64.abs() @ W64.abs().T).max()))
+    zt = (h64 * W[y.long()].double()).sum(1)
+    # a logit is a few sums of fp32; the sum over the vocabulary has at most 2^14 + 2^11 steps in one thread, each
+    # rounded twice where two sums are joined
+    dz = 2.0 ** -19 * most
+    sums = (2 ** 14 + 2 ** 11) * 2.0 ** -23
+    assert ((lse - total).abs() <= dz + sums).all() and ((loss - (total - zt)).abs() <= 2 * dz + sums).all()
+    want_h, size_h = torch.zeros_like(h64), torch.zeros_like(h64)
+    rel = 2.0 ** -8 + 3 * dz + sums
+    for a in range(0, V, step):
+        W64 = W[a:a + step].double()
+        G = torch.exp(h64 @ W64.T - total[:, None])
+        for i in range(n):
+            if a <= int(y[i]) < a + step:
+                G[i, int(y[i]) - a] -= 1
+        G *= dl.double()[:, None]
+        want_h += G @ W64
+        size_h += G.abs() @ W64.abs()
+        want, size = G.T @ h64, G.abs().T @ h64.abs()
+        assert ((dW[a:a + step] - want).abs() <= rel * (1 + 2.0 ** -8) * size + 2.0 ** -8 * want.abs() + 1e-38).all()
+    # dh: 74 parts of a piece of 409600 columns, 656 pieces: 346 sums of 16 products, 656 and 74 sums of those
+    assert ((dh - want_h).abs() <= (rel + 1100 * 2.0 ** -23) * size_h + 2.0 ** -8 * want_h.abs()).all()
