@@ -698,6 +698,7 @@ dg_status dg_adamw_step(const dg_adamw_params* p, const dg_adamw_tensor* tensors
     if (!(p->lr >= 0) || !std::isfinite(p->lr) || !(p->beta1 >= 0 && p->beta1 < 1) ||
         !(p->beta2 >= 0 && p->beta2 < 1) || !(p->eps >= 0) || !std::isfinite(p->eps))
         return DG_EINVAL;
+    if (p->eps > 0 && p->eps < 0x1p-126) return DG_EINVAL;      // div_sfu takes a subnormal for 0
     if (!p->step_dev && p->step < 1) return DG_EINVAL;
     if (p->state_bits != 8 && p->state_bits != 32) return DG_EINVAL;
     if ((p->param_type != DG_FP32 && p->param_type != DG_BF16) || (p->grad_type != DG_FP32 && p->grad_type != DG_BF16))

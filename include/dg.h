@@ -379,7 +379,9 @@ enum { DG_INT32 = 0, DG_INT64 = 1 };
 /*
  * Cross entropy of a head W [vocab, hidden] at n positions.  Limits: n >= 0, vocab >= 1,
  * temperature > 0 and finite, its reciprocal too, scratch_bytes >= 0 (DG_EINVAL otherwise);
- * hidden a multiple of 8 up to 65536, n up to 2^22, vocab up to 2^28 (DG_EUNSUPPORTED otherwise).
+ * hidden a multiple of 8 up to 65536, n up to 2^22, vocab up to 2^28, and fewer than 2^31 tiles of
+ * 256 x 256 logits (DG_EUNSUPPORTED otherwise).  What a call writes overlaps neither what it
+ * reads nor the workspace, but where it says so.
  */
 typedef struct {
     int n;                  /* positions */
@@ -445,7 +447,7 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
  * Per element, with g' = grad_scale * g and step t:
  *   m <- beta1 m + (1 - beta1) g'      v <- beta2 v + (1 - beta2) g'^2
  *   p <- p (1 - lr wd) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
- * in fp32.  state_bits 32: m and v are fp32 [n].  state_bits 8: m and v are E4M3 codes [n]
+ * in fp32 (an update's numerator below 2^-126 counts as 0).  state_bits 32: m and v are fp32 [n].  state_bits 8: m and v are E4M3 codes [n]
  * of m and of sqrt(v), with one power-of-two exponent (int8) for every 256 consecutive
  * elements, value = decode(code) 2^exp; the exponent is the smallest with max |x| 2^-exp <= 448
  * (0 for a block of zeros, at least -100), and codes are rounded between their two E4M3
@@ -464,7 +466,7 @@ dg_status dg_xent_backward(const dg_xent_params* p, const void* h_dev, const voi
  * step can be replayed with other values.
  */
 typedef struct {
-    double lr, beta1, beta2, eps;   /* lr, eps >= 0; betas in [0, 1) */
+    double lr, beta1, beta2, eps;   /* lr >= 0; eps 0 or at least 2^-126; betas in [0, 1) */
     uint64_t seed;
     const float* lr_dev;
     const int32_t* step_dev;

@@ -121,3 +121,13 @@ def test_the_update_keeps_to_registers_but_for_a_few_words(tmp_path):
         of_bf16 = "kernelI13__nv_bfloat16" in name
         state8 = name.split("Lb")[1][0] == "1"
         assert max(map(int, spills)) <= (24 if of_bf16 and state8 else 0), name
+
+
+@pytest.mark.parametrize("eps", [1e-46, 1e-40, 2.0 ** -127])
+def test_an_eps_below_the_normal_range_is_refused(dg, eps):
+    """The quotient takes a subnormal denominator for 0: an element without moments would become 0 / 0."""
+    from discrete_diffusion_decoding_b200._abi import DG_EINVAL, lib
+    z = [torch.zeros(5) for _ in range(4)]
+    p = dg.adamw_params(eps=eps, param_type=0, grad_type=0)
+    T = dg.AdamWTensors(z[:1], z[1:2], z[2:3], z[3:])
+    assert lib().dg_adamw_step(ctypes.byref(p), T.table, 1, None) == DG_EINVAL
