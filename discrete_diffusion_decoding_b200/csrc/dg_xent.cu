@@ -36,6 +36,7 @@
 #include <cmath>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "../../include/dg.h"
@@ -64,12 +65,14 @@ constexpr int kPackRows = 8;               // rows a CTA of the gather looks at 
 // the rows of dW that are a target's the remainders times their positions' hidden states.  The products keep those
 // rows of dW unrounded beside it for that (Packed::dw_rows; Packed::first_of tells them, from the launch before the
 // first of dW).  The gradients are then as far from the 64-bit result as their own type's rounding, 0.0017 of their
-// norm instead of 0.0024, for 0.6 us more at 256 positions, V = 4096, d = 128 (backward 27.5 us) and 0.3 to 0.8 % of
-// the larger ones.  (A search through the targets by each item's epilogue instead of first_of: 5 % at 256 positions
-// of V = 262144.)
+// norm instead of 0.0024, for 0.9 us more at 256 positions, V = 4096, d = 128 (backward 27.6 us) and at most 1 % of the
+// larger ones.  (A search through the targets by each item's epilogue instead of first_of: 5 % at 256 positions of
+// V = 262144.  One CTA for a target instead of one for each part of its row: 15.2 instead of 14.2 ms where all of
+// 4096 positions have one.)
 constexpr int kNoPosition = 0x7fffffff;
 constexpr int kRestScan = 2048;            // targets that a CTA looks at together there
 constexpr int kRestList = 2 * kRestScan;   // positions of one target in hand there
+constexpr int kRestCols = 256;             // columns of a part of a row there, where many positions have one target
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
@@ -1159,44 +1162,56 @@ struct FinishArgs {
     int dw_fp32, dw_accumulate;
 };
 
-// The remainders of `count` listed positions times their hidden states and the row's sums so far, 4 columns a thread:
-// the new sums, or (kLast) the row of dW.  Where many positions meet a small d, several threads share a column and
-// take the positions in turn.
+// The remainders of `count` listed positions times their hidden states and the row's sums so far, for the columns of
+// part `part` of the row, 4 a thread: the new sums, or (kLast) the row of dW.  With few positions a part is 1024
+// columns; with many it is kRestCols, and the threads that share a column take the positions in turn.
 template <bool kLast>
-__device__ __forceinline__ void add_rest(const FinishArgs& a, float* sums, int y, const int* list, int count,
-                                         float4* shared) {
-    const int vecs = a.d / 4, wide = min(vecs, 256), shares = count < 8 ? 1 : 256 / wide;
+__device__ __forceinline__ void add_rest(const FinishArgs& a, float* sums, int y, const int* list, int count, bool many,
+                                         int part, float4* shared) {
+    const int wide = min(a.d / 4, many ? kRestCols / 4 : 256), shares = many ? 256 / wide : 1;
     const int share = threadIdx.x / wide, own = threadIdx.x - share * wide;
-    for (int v0 = 0; v0 < vecs; v0 += wide) {
-        const int c = (v0 + own) * 4;
-        const bool live = share < shares && c < a.d, writes = live && share == 0;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (writes) x = *reinterpret_cast<const float4*>(sums + c);
-        if (live) {
-#pragma unroll 4
-            for (int k = share; k < count; k += shares) {
-                const float t = a.pk.trest[list[k]];
-                const uint2 h = *reinterpret_cast<const uint2*>(a.pk.h + static_cast<long long>(list[k]) * a.d + c);
-                x.x = fmaf(t, __uint_as_float(h.x << 16), x.x);
-                x.y = fmaf(t, __uint_as_float(h.x & 0xFFFF0000u), x.y);
-                x.z = fmaf(t, __uint_as_float(h.y << 16), x.z);
-                x.w = fmaf(t, __uint_as_float(h.y & 0xFFFF0000u), x.w);
+    const int c = (part * wide + own) * 4;
+    const bool live = share < shares && c < a.d, writes = live && share == 0;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (writes) x = *reinterpret_cast<const float4*>(sums + c);
+    if (live) {
+        int k = share;
+        auto add = [&](auto batch) {          // so many loads in flight
+            constexpr int n = decltype(batch)::value;
+            float t[n];
+            uint2 h[n];
+#pragma unroll
+            for (int q = 0; q < n; ++q) {
+                const int at = list[k + q * shares];
+                t[q] = __ldg(a.pk.trest + at);
+                h[q] = __ldg(reinterpret_cast<const uint2*>(a.pk.h + static_cast<long long>(at) * a.d + c));
             }
-        }
-        if (shares > 1) {
-            shared[threadIdx.x] = x;
-            __syncthreads();
-            for (int k = 1; writes && k < shares; ++k) {
-                const float4 o = shared[k * wide + own];
-                x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
+#pragma unroll
+            for (int q = 0; q < n; ++q) {
+                x.x = fmaf(t[q], __uint_as_float(h[q].x << 16), x.x);
+                x.y = fmaf(t[q], __uint_as_float(h[q].x & 0xFFFF0000u), x.y);
+                x.z = fmaf(t[q], __uint_as_float(h[q].y << 16), x.z);
+                x.w = fmaf(t[q], __uint_as_float(h[q].y & 0xFFFF0000u), x.w);
             }
-            __syncthreads();
+            k += n * shares;
+        };
+        while (k + 11 * shares < count) add(std::integral_constant<int, 12>());
+        while (k + 2 * shares < count) add(std::integral_constant<int, 3>());
+        while (k < count) add(std::integral_constant<int, 1>());
+    }
+    if (shares > 1) {
+        shared[threadIdx.x] = x;
+        __syncthreads();
+        for (int k = 1; writes && k < shares; ++k) {
+            const float4 o = shared[k * wide + own];
+            x = make_float4(x.x + o.x, x.y + o.y, x.z + o.z, x.w + o.w);
         }
-        if (!writes) continue;
-        if constexpr (!kLast) {
-            *reinterpret_cast<float4*>(sums + c) = x;
-            continue;
-        }
+        __syncthreads();
+    }
+    if (!writes) return;
+    if constexpr (!kLast) {
+        *reinterpret_cast<float4*>(sums + c) = x;
+    } else {
         const long long to = static_cast<long long>(y) * a.d + c;
         if (a.dw_fp32) {
             float4* out = reinterpret_cast<float4*>(static_cast<float*>(a.dw) + to);
@@ -1217,17 +1232,21 @@ __device__ __forceinline__ void add_rest(const FinishArgs& a, float* sums, int y
     }
 }
 
-// dW's row of position `at`'s target, by a CTA, where `at` is the first of it: the remainders of all positions of that
-// target in their order.  One barrier for each kRestScan targets; `turn` alternates the words that the warps exchange.
+// dW's row of position `at`'s target, by a CTA: the remainders of all positions of that target, listed in their order.
+// The row's parts go round among the CTAs of the target's first positions.  One barrier for each kRestScan targets;
+// `turn` alternates the words that the warps exchange.
 __device__ __forceinline__ void finish_dw_row(const FinishArgs& a, int at, int rows, int& turn) {
-    __shared__ int list[kRestList];
+    __shared__ int list[kRestList], rank_of_at;
     __shared__ int of_warp[2][8];         // how many positions of this target each warp sees
     __shared__ float4 shared[256];
     const int y = a.pk.target[at], tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (y < 0 || a.pk.first_of[y] != at) return;      // outside the vocabulary all of dW is NaN already
-    float* sums = a.pk.dw_rows + static_cast<long long>(at) * a.d;
-    int count = 0;
-    for (int base = at & ~3; base < rows; base += kRestScan, turn ^= 1) {
+    if (y < 0) return;                // outside the vocabulary: all of dW is NaN already
+    const int first = a.pk.first_of[y], most_parts = (a.d + kRestCols - 1) / kRestCols;
+    if (first != at && most_parts == 1) return;
+    float* sums = a.pk.dw_rows + static_cast<long long>(first) * a.d;
+    int seen = 0, count = 0;              // positions of this target, and those listed
+    for (int base = first & ~3; base < rows; base += kRestScan, turn ^= 1) {
+        if (base <= at && seen >= most_parts) return;         // no part is left for `at`
         const int i = base + tid * 8;
         uint32_t hits = 0;
 #pragma unroll
@@ -1252,6 +1271,10 @@ __device__ __forceinline__ void finish_dw_row(const FinishArgs& a, int at, int r
         }
         if (lane == 0) of_warp[turn][warp] = all;
         __syncthreads();
+        if (base > at && rank_of_at >= most_parts) {
+            turn ^= 1;
+            return;
+        }
         all = 0;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
@@ -1259,16 +1282,24 @@ __device__ __forceinline__ void finish_dw_row(const FinishArgs& a, int at, int r
             if (w < warp) before += o;
             all += o;
         }
-        if (count + all > kRestList) {
-            add_rest<false>(a, sums, y, list, count, shared);
+        if (count + all > kRestList) {        // `at` has its part: there are more positions than parts
+            add_rest<false>(a, sums, y, list, count, true, rank_of_at, shared);
             __syncthreads();
             count = 0;
         }
-        for (; hits; hits &= hits - 1) list[count + before++] = i + __ffs(hits) - 1;
+        for (; hits; hits &= hits - 1) {
+            const int k = i + __ffs(hits) - 1;
+            if (k == at) rank_of_at = seen + before;
+            list[count + before++] = k;
+        }
+        seen += all;
         count += all;
     }
     __syncthreads();
-    add_rest<true>(a, sums, y, list, count, shared);
+    const bool many = seen >= 8;
+    const int parts = many ? most_parts : (a.d + 1023) / 1024;
+    for (int part = rank_of_at; part < parts; part += seen)
+        add_rest<true>(a, sums, y, list, count, many, part, shared);
 }
 
 // dh rows: the slabs' sum and the target's remainder in bf16 at the original positions; the rows of dW that are a

@@ -69,7 +69,8 @@ def test_the_targets_entry_of_g_is_not_rounded_away(dg, n, V, d, kept, scratch):
 
 
 @pytest.mark.parametrize("n,V,d,dtype", [(300, 40, 64, torch.float32), (3000, 700, 72, torch.bfloat16),
-                                         (2500, 5, 2104, torch.float32), (9000, 300, 8, torch.bfloat16)])
+                                         (2500, 5, 2104, torch.float32), (9000, 300, 8, torch.bfloat16),
+                                         (20, 6, 2104, torch.bfloat16), (10000, 30, 520, torch.float32)])
 @pytest.mark.parametrize("add", [0, 1])
 def test_many_positions_of_one_target(dg, n, V, d, dtype, add):
     """Half of the positions have one target, more than the last launch holds of one at a time; equal calls give equal
