@@ -917,10 +917,16 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
 // and the positions its 16 or 32 columns, so that the tensor core does not multiply 256 rows for one.  That costs
 // power, and with it the clock that the reads from memory need.  Each CTA streams its rows of W through a ring of
 // its own and each epilogue thread keeps a running (maximum, sum) of every position over the vocabulary rows it
-// sees.  At V = 262144, d = 2816, heads in turn: 243 us for 1 position (6.1 TB/s; the kernel above 342), 246 for
-// 16 (323), 265 to 280 for 32 (332).  With 64 columns the final sums over the lanes cost more than is saved on
+// sees.  At V = 262144, d = 2816, heads in turn: 246 us for 1 position (6.0 TB/s; the kernel above 342), 248 for
+// 16 (323), 254 for 32 (332).  With 64 columns the final sums over the lanes cost more than is saved on
 // smaller heads (n = 64, V = 5000: 47 us against 36; n = 33, V = 50000, d = 1000: 53 against 46).
+// The tensor core cuts its running sum off at every 16 products, which puts up to d / 16 units in the last place on a
+// logit, all to one side.  Each sum is therefore made in kFewParts parts with an accumulator each, which the epilogue
+// adds: an eighth of that (V = 262144, d = 2816, 1 position: lse off by 0.2 to 1.5e-7 of itself instead of 2 to
+// 3.4e-7, in 246 us instead of 243).
 constexpr int kFewRows = 32;               // positions at most
+constexpr int kFewParts = 8;
+constexpr int kFewAcc = kFewParts * kFewRows;   // TMEM columns of a tile's accumulators, of which there are two
 constexpr int kFewStages = 12;
 constexpr int kFewRingBytes = 220 * 1024;
 constexpr int kFewSmemBytes = kFewRingBytes + 1024;
@@ -937,7 +943,7 @@ struct FewArgs {
 
 template <int kColumns>
 __device__ __forceinline__ void few_epilogue(const FewArgs& a, uint32_t tmem, uint64_t* acc_full, uint64_t* acc_free,
-                                             const int* target, int* abort_flag, int rows, int tiles) {
+                                             const int* target, int* abort_flag, int rows, int tiles, int parts) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & 127;
     float m[kColumns], l[kColumns];
 #pragma unroll
@@ -951,12 +957,19 @@ __device__ __forceinline__ void few_epilogue(const FewArgs& a, uint32_t tmem, ui
         if (group_any(0, !mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag, a.pk.err, kErrAccFull, a.wait_ns)))
             return;
         tc_fence_after();
-        uint32_t r[kColumns];
+        const uint32_t acc = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * kFewAcc;
+        float sum[kColumns];
 #pragma unroll
-        for (int c = 0; c < kColumns; c += 16)
-            tmem_ld16(tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + buf * kFewRows + c,
-                      *reinterpret_cast<uint32_t(*)[16]>(&r[c]));
-        tmem_wait_ld();
+        for (int c = 0; c < kColumns; ++c) sum[c] = 0.f;
+        for (int part = 0; part < parts; ++part) {
+            uint32_t r[kColumns];
+#pragma unroll
+            for (int c = 0; c < kColumns; c += 16)
+                tmem_ld16(acc + part * kFewRows + c, *reinterpret_cast<uint32_t(*)[16]>(&r[c]));
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kColumns; ++c) sum[c] += __uint_as_float(r[c]);
+        }
         tc_fence_before();
         group_bar(0);
         if (row == 0) mbar_arrive(&acc_free[buf]);
@@ -964,7 +977,7 @@ __device__ __forceinline__ void few_epilogue(const FewArgs& a, uint32_t tmem, ui
         if (v >= a.vocab) continue;
 #pragma unroll
         for (int c = 0; c < kColumns; ++c) {
-            const float z = v == target[c] ? -INFINITY : __uint_as_float(r[c]) * a.scale_log2;
+            const float z = v == target[c] ? -INFINITY : sum[c] * a.scale_log2;
             const float m2 = fmaxf(m[c], z), ref = m2 == -INFINITY ? 0.f : m2;
             l[c] = l[c] * exp2_sfu(m[c] - ref) + exp2_sfu(z - ref);
             m[c] = m2;
@@ -1008,7 +1021,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
         abort_flag = 0;
     }
     if (warp == 1) {
-        tmem_alloc(&tmem_base, 2 * kFewRows);
+        tmem_alloc(&tmem_base, 2 * kFewAcc);
         tmem_relinquish();
     }
     griddep_launch();
@@ -1028,6 +1041,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
     const int kbs = (a.d + kK - 1) / kK;
     const int stage_bytes = kOperand + a.columns * 128;
     const int stages = min(kFewStages, kFewRingBytes / stage_bytes);
+    const int per_part = (kbs + kFewParts - 1) / kFewParts, parts = (kbs + per_part - 1) / per_part;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -1072,7 +1086,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
                     !mbar_wait(&acc_free[buf], ((n >> 1) - 1) & 1, &abort_flag, err, kErrAccFree, a.wait_ns))
                     break;
                 tc_fence_after();
-                for (int k = 0; k < kbs; ++k, ++used) {
+                const uint32_t acc = tmem + buf * kFewAcc;
+                for (int k = 0, part = 0, in_part = 0; k < kbs; ++k, ++used) {
                     const uint32_t s = used % stages;
                     if (!mbar_wait(&full[s], (used / stages) & 1, &abort_flag, err, kErrFull, a.wait_ns)) {
                         ok = false;
@@ -1082,9 +1097,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
                     const uint32_t sa = smem_u32(ring + s * stage_bytes), sb = sa + kOperand;
 #pragma unroll
                     for (int kk = 0; kk < kK / 16; ++kk)
-                        umma_ss(tmem + buf * kFewRows, smem_desc(sa + kk * 32, 16, 1024, kSwizzle128B),
-                                smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B), idesc, (k | kk) != 0 ? 1u : 0u);
+                        umma_ss(acc + part * kFewRows, smem_desc(sa + kk * 32, 16, 1024, kSwizzle128B),
+                                smem_desc(sb + kk * 32, 16, 1024, kSwizzle128B), idesc, (in_part | kk) != 0 ? 1u : 0u);
                     umma_commit(&empty[s]);
+                    if (++in_part == per_part) {
+                        in_part = 0;
+                        ++part;
+                    }
                 }
                 if (ok) umma_commit(&acc_full[buf]);
             }
@@ -1098,13 +1117,13 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
             }
         }
     } else if (warp >= 4) {
-        if (a.columns == 16) few_epilogue<16>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles);
-        else few_epilogue<32>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles);
+        if (a.columns == 16) few_epilogue<16>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles, parts);
+        else few_epilogue<32>(a, tmem, acc_full, acc_free, target, &abort_flag, rows, tiles, parts);
     }
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();
-    if (warp == 1) tmem_dealloc(tmem, 2 * kFewRows);
+    if (warp == 1) tmem_dealloc(tmem, 2 * kFewAcc);
 }
 
 // ------------------------------------------------------------------ merges

@@ -492,3 +492,26 @@ def test_the_largest_vocabulary(dg, n):
         assert ((dW[a:a + step] - want).abs() <= rel * (1 + 2.0 ** -8) * size + 2.0 ** -8 * want.abs() + 1e-38).all()
     # dh: 74 parts of a piece of 409600 columns, 656 pieces: 346 sums of 16 products, 656 and 74 sums of those
     assert ((dh - want_h).abs() <= (rel + 1100 * 2.0 ** -23) * size_h + 2.0 ** -8 * want_h.abs()).all()
+
+
+# ------------------------------------------------------------------ truncated sums
+@pytest.mark.parametrize("n", [1, 17, 32])
+def test_long_sums_of_few_positions_are_cut_into_parts(dg, n):
+    """Products of one sign, whose running sum the tensor core cuts off at every 16: with the sum in eight parts the
+    logits are off by an eighth of that."""
+    V, d = 1000, 8192
+    g = torch.Generator().manual_seed(n)
+    W = ((0.5 + torch.rand(V, d, generator=g)) / 256).bfloat16()
+    h = (0.5 + torch.rand(n, d, generator=g)).bfloat16()
+    y = torch.randint(0, V, (n,), generator=g).int()
+    p = dg.xent_params(n, V, d)
+    loss, lse = torch.empty(n, device="cuda"), torch.empty(n, device="cuda")
+    dg.dg_xent_forward(p, h.cuda(), W.cuda(), y.cuda(), loss, lse, dg.XentWorkspace(p, backward=False))
+    want, want_lse = xent.cross_entropy(h.double().numpy(), W.double().numpy(), y.numpy())
+    z = (h.double() @ W.double().T).max()
+    # a part has 64 steps of 16 products and loses at most 2^-23 of its running sum at each, half of its sum on
+    # average as all products have one sign; the parts' sum has 8 roundings.  The exponentials and their sum in log2
+    # units: 2^-20; lse's own rounding
+    tol = float((64 / 2 + 8) * 2.0 ** -23 * z + 2.0 ** -20 + 2.0 ** -23 * want_lse.max())
+    assert np.all(np.abs(lse.cpu().double().numpy() - want_lse) <= tol)
+    assert np.all(np.abs(loss.cpu().double().numpy() - want) <= 2 * tol)
