@@ -17,9 +17,10 @@
 // vocabulary] tiles whose epilogue keeps a (maximum, sum) per row and half tile, and a merge.
 // Backward: launch k computes G for piece k + 1 of the vocabulary (the same product, G written in
 // bf16, the operand type of the two products that read it: each entry is off by at most 2^-8 of
-// itself, as an output in bf16 is; see kRestList for the target's) and both gradients' tiles for piece k, so that the tails, the
-// memory-bound and the compute-bound tiles of the three overlap; dW is written once, dh is added in
-// fp32 to slabs that the last launch sums, rounds and scatters.
+// itself, as an output in bf16 is; see kRestList for the target's) and both gradients' tiles for
+// piece k, so that the tails, the memory-bound and the compute-bound tiles of the three overlap; dW
+// is written once, but for its targets' rows, and dh is added in fp32 to slabs that the last launch
+// sums, rounds and scatters.
 //
 // The products run on CTA pairs (cta_group::2 UMMA, 256 x 256 tiles, K in stages of 64).  An item is two
 // tiles side by side that share A: 48 KB a stage and CTA for 1024 tensor cycles, where one tile takes 32 KB for
@@ -107,7 +108,8 @@ struct Packed {
     float* tcoef;        // backward: the target's entry of G
     float* trest;        // and what its rounding to bf16 leaves out
     int32_t* first_of;   // backward, dW: [vocab] the first position of each row of W that is a target, or kNoPosition
-    float* dw_rows;      // backward: [n, d]; row i: dW's row of target i before its rounding, where i is that target's first
+    float* dw_rows;      // backward: dW's rows of targets before their rounding, of target y with first position i in
+    int dw_by_position;  // row i of [n, d] where there are fewer positions than rows of W, else in row y of [vocab, d]
     __nv_bfloat16* h;    // [rounded up to 256 rows, d]; zeros up to a multiple of 64 rows
     uint32_t* tickets;   // one counter of items for each launch of products
     int n_tickets;
@@ -545,7 +547,7 @@ __device__ __forceinline__ void dw_epilogue(const GemmArgs& a, int n0, uint32_t 
         for (int k = 0; k < kHalf; ++k) r[k] = 0;
     }
     if (of_target) {
-        float* to = a.pk.dw_rows + static_cast<long long>(target_first) * a.d + n0;
+        float* to = a.pk.dw_rows + static_cast<long long>(a.pk.dw_by_position ? target_first : v) * a.d + n0;
 #pragma unroll
         for (int c = 0; c < kHalf; c += 4)
             if (n0 + c < a.d)
@@ -1262,7 +1264,7 @@ __device__ __forceinline__ void finish_dw_row(const FinishArgs& a, int at, int r
     if (y < 0) return;                // outside the vocabulary: all of dW is NaN already
     const int first = a.pk.first_of[y], most_parts = (a.d + kRestCols - 1) / kRestCols;
     if (first != at && most_parts == 1) return;
-    float* sums = a.pk.dw_rows + static_cast<long long>(first) * a.d;
+    float* sums = a.pk.dw_rows + static_cast<long long>(a.pk.dw_by_position ? first : y) * a.d;
     int seen = 0, count = 0;              // positions of this target, and those listed
     for (int base = first & ~3; base < rows; base += kRestScan, turn ^= 1) {
         if (base <= at && seen >= most_parts) return;         // no part is left for `at`
@@ -1376,6 +1378,7 @@ struct XentPlan {
     int rows_alloc, v_tiles, d_tiles, pairs;
     int piece, pieces;       // columns per piece of the backward, and their number
     int splits, kb_per_split;
+    int dw_by_position;
     size_t err, row, target, lse2, coef, tcoef, trest, first_of, dw_rows, zt2, h, tickets, part, g, slab, total;
 };
 
@@ -1448,7 +1451,8 @@ dg_status plan_xent(const dg_xent_params* p, bool backward, XentPlan* out) {
         q.g = take((q.pieces > 1 ? 4 : 2) * n * q.piece);
         q.slab = take(4 * n * p->hidden * q.splits);
         q.first_of = take(4 * static_cast<size_t>(p->vocab));
-        q.dw_rows = take(4 * static_cast<size_t>(p->n) * p->hidden);
+        q.dw_by_position = p->n < p->vocab;
+        q.dw_rows = take(4 * static_cast<size_t>(q.dw_by_position ? p->n : p->vocab) * p->hidden);
     }
     q.total = o;
     *out = q;
@@ -1475,6 +1479,7 @@ Packed packed_of(const XentPlan& q, void* ws) {
     k.trest = at<float>(ws, q.trest);
     k.first_of = at<int32_t>(ws, q.first_of);
     k.dw_rows = at<float>(ws, q.dw_rows);
+    k.dw_by_position = q.dw_by_position;
     k.h = at<__nv_bfloat16>(ws, q.h);
     return k;
 }
