@@ -66,7 +66,7 @@ constexpr int kPackRows = 8;               // rows a CTA of the gather looks at 
 // the rows of dW that are a target's the remainders times their positions' hidden states.  The products keep those
 // rows of dW unrounded beside it for that (Packed::dw_rows; Packed::first_of tells them, from the launch before the
 // first of dW).  The gradients are then as far from the 64-bit result as their own type's rounding, 0.0017 of their
-// norm instead of 0.0024, for 0.9 us more at 256 positions, V = 4096, d = 128 (backward 27.6 us) and at most 1 % of the
+// norm instead of 0.0024, for 0.5 us more at 256 positions, V = 4096, d = 128 (backward 27.6 us) and at most 1 % of the
 // larger ones.  (A search through the targets by each item's epilogue instead of first_of: 5 % at 256 positions of
 // V = 262144.  One CTA for a target instead of one for each part of its row: 15.2 instead of 14.2 ms where all of
 // 4096 positions have one.)
@@ -1326,8 +1326,8 @@ __device__ __forceinline__ void finish_dw_row(const FinishArgs& a, int at, int r
 // dh rows: the slabs' sum and the target's remainder in bf16 at the original positions; the rows of dW that are a
 // target's (see kRestList).  After a wait that ran out both gradients are NaN.
 __global__ void __launch_bounds__(256) dg_xent_finish_kernel(const __grid_constant__ FinishArgs a) {
-    griddep_launch();
     griddep_wait();
+    griddep_launch();         // not before: the next kernel's CTAs beside these cost 2.7 of 47 us at 256 x 4096 x 128
     const bool bad = *a.pk.err != 0;
     const int rows = *a.pk.count, d = a.d;
     if (bad && a.dw) {
