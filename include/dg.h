@@ -426,8 +426,9 @@ dg_status dg_xent_forward(const dg_xent_params* p, const void* h_dev, const void
  * Gradients of sum_i dloss_i loss_i, from the forward's loss and lse of the same inputs:
  *   G[i,v] = dloss_i / T (e^{z[i,v] - lse_i} - [v = y_i]),  dh = G W,  dW = G^T h
  * with the logits computed again, a piece of the vocabulary at a time; G is rounded to
- * bf16 for the two products, whose sums are fp32; what the rounding of the target's entry
- * leaves out is added to both.  Ignored positions and those with
+ * bf16 for the two products; what the rounding of the target's entry leaves out is added to
+ * both.  All products sum in fp32 as the tensor core does, which cuts a running sum off
+ * towards zero at every 16 products.  Ignored positions and those with
  * dloss_i = 0 get a zero row of dh and no part in dW, whatever their hidden states hold.
  * An invalid target (see dg_xent_forward) makes its row of dh and all of dW NaN.
  *   dloss_dev: [n] float

@@ -131,3 +131,20 @@ def test_an_eps_below_the_normal_range_is_refused(dg, eps):
     p = dg.adamw_params(eps=eps, param_type=0, grad_type=0)
     T = dg.AdamWTensors(z[:1], z[1:2], z[2:3], z[3:])
     assert lib().dg_adamw_step(ctypes.byref(p), T.table, 1, None) == DG_EINVAL
+
+
+def test_states_saved_without_counts(dg):
+    """A state_dict from before each parameter had a count takes the step count for all; another number of counts is
+    another optimizer's."""
+    ps = [torch.zeros(5), torch.zeros(7, dtype=torch.bfloat16)]
+    opt = dg.AdamW(ps)
+    state = opt.state_dict()
+    state["steps"] = 7
+    saved = dict(state)
+    del saved["counts"]
+    opt.load_state_dict(saved)
+    assert opt.steps == 7 and opt.counts == [7, 7]
+    opt.load_state_dict(dict(state, counts=[7, 3]))
+    assert opt.counts == [7, 3]
+    with pytest.raises(dg.DgError):
+        opt.load_state_dict(dict(state, counts=[7]))
