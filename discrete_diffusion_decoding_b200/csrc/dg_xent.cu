@@ -925,9 +925,13 @@ __global__ void __launch_bounds__(kXThreads, 1) dg_xent_gemm_kernel(const __grid
 // The tensor core cuts its running sum off at every 16 products, which puts up to d / 16 units in the last place on a
 // logit, all to one side.  Each sum is therefore made in kFewParts parts with an accumulator each, which the epilogue
 // adds: an eighth of that (V = 262144, d = 2816, 1 position: lse off by 0.2 to 1.5e-7 of itself instead of 2 to
-// 3.4e-7, in 246 us instead of 243).
+// 3.4e-7, in 246 us instead of 243).  The backward's logits are not made in parts, and its softmax is as far from
+// adding up to 1 as they are from the forward's: past kFewPartStages one part again.  With products of one sign, logits
+// of 32 and 17 positions: d = 4096 loss 1.1e-6 and dh 1.7e-3 of their norms off in parts, 3.7e-5 and 1.5e-3 in one;
+// d = 8192 3.8e-6 and 3.0e-3, 1.1e-4 and 1.5e-3; d = 65536 dh 3.5e-2 and 1.5e-3.
 constexpr int kFewRows = 32;               // positions at most
 constexpr int kFewParts = 8;
+constexpr int kFewPartStages = 64;
 constexpr int kFewAcc = kFewParts * kFewRows;   // TMEM columns of a tile's accumulators, of which there are two
 constexpr int kFewStages = 12;
 constexpr int kFewRingBytes = 220 * 1024;
@@ -1043,7 +1047,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) dg_xent_few_kernel(const __gri
     const int kbs = (a.d + kK - 1) / kK;
     const int stage_bytes = kOperand + a.columns * 128;
     const int stages = min(kFewStages, kFewRingBytes / stage_bytes);
-    const int per_part = (kbs + kFewParts - 1) / kFewParts, parts = (kbs + per_part - 1) / per_part;
+    const int per_part = kbs <= kFewPartStages ? (kbs + kFewParts - 1) / kFewParts : kbs;
+    const int parts = (kbs + per_part - 1) / per_part;
 
     if (warp == 0) {
         if (lane == 0) {
